@@ -1,4 +1,5 @@
-"""ctypes binding of liblora_mlp.so (include/lora_mlp.h, lora_linear.h, lora_rmsnorm.h, lora_ce.h).
+"""ctypes binding of liblora_mlp.so (include/lora_mlp.h, lora_linear.h, lora_rmsnorm.h, lora_ce.h; lora_step.h,
+lora_embedding.h).
 
 Argument marshalling only: every step of the MLP runs in the library's CUDA
 kernels.  Loading fails loudly if the shared library has not been built.
@@ -65,6 +66,20 @@ SYMBOLS = (
     "lora_ce_backward_reduced",
     "lora_ce_device_status",
 )
+
+# Every symbol of the operators around the dense layers: lora_step.h and lora_embedding.h.
+STEP_SYMBOLS = (
+    "lora_step_device_status",
+    "lora_step_timing_enable",
+    "lora_step_timing_collect",
+    "lora_step_launch_count",
+    "lora_embedding_forward",
+    "lora_embedding_sizes",
+    "lora_embedding_backward",
+)
+
+EMBEDDING_GRAD_BF16 = 0
+EMBEDDING_GRAD_FP32 = 1
 
 
 class Shape(ctypes.Structure):
@@ -163,6 +178,17 @@ def lib() -> ctypes.CDLL:
             L.lora_ce_backward_reduced.argtypes = [ctypes.POINTER(CEShape), vp, vp, vp, vp, vp, vp, vp]
             L.lora_mlp_workspace_size.argtypes = [ctypes.POINTER(Shape), ctypes.POINTER(sz), ctypes.POINTER(sz)]
             L.lora_ce_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
+            L.lora_step_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
+            L.lora_step_timing_enable.argtypes = [ctypes.c_int]
+            L.lora_step_timing_collect.argtypes = L.lora_mlp_timing_collect.argtypes
+            L.lora_step_launch_count.argtypes = []
+            L.lora_embedding_forward.argtypes = [i64, i64, i64, ctypes.c_float, vp, vp, vp, vp]
+            L.lora_embedding_sizes.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
+            L.lora_embedding_backward.argtypes = [i64, i64, i64, ctypes.c_float, i64, ctypes.c_int, vp, vp, vp, vp, sz,
+                                                  vp]
+            for name in STEP_SYMBOLS:
+                getattr(L, name).restype = ctypes.c_int
+            L.lora_step_launch_count.restype = ctypes.c_int64
             L.lora_mlp_launch_count.argtypes = []
             L.lora_mlp_launch_count.restype = ctypes.c_int64
             for name in ("lora_mlp_sizes", "lora_mlp_forward", "lora_mlp_forward_noalloc", "lora_mlp_backward",
@@ -250,13 +276,19 @@ def device_status(stream) -> int:
 
 def timing_enable(on: bool) -> None:
     check(lib().lora_mlp_timing_enable(1 if on else 0), "lora_mlp_timing_enable")
+    check(lib().lora_step_timing_enable(1 if on else 0), "lora_step_timing_enable")
 
 
 def timing_collect(max_records: int = 4096):
-    buf = (KernelTime * max_records)()
-    n = ctypes.c_int(0)
-    check(lib().lora_mlp_timing_collect(buf, max_records, ctypes.byref(n)), "lora_mlp_timing_collect")
-    return [(buf[i].name.decode(), float(buf[i].ms)) for i in range(min(n.value, max_records))]
+    """(name, ms) of every launch recorded: those of the dense layers, norms and losses in launch order, then those
+    of the operators of lora_step.h in theirs."""
+    got = []
+    for name in ("lora_mlp_timing_collect", "lora_step_timing_collect"):
+        buf = (KernelTime * max_records)()
+        n = ctypes.c_int(0)
+        check(getattr(lib(), name)(buf, max_records, ctypes.byref(n)), name)
+        got += [(buf[i].name.decode(), float(buf[i].ms)) for i in range(min(n.value, max_records))]
+    return got
 
 
 def debug_force_timeout(enable: bool, wait_cycles: int = 0) -> None:
@@ -264,7 +296,13 @@ def debug_force_timeout(enable: bool, wait_cycles: int = 0) -> None:
 
 
 def launch_count() -> int:
-    return int(lib().lora_mlp_launch_count())
+    return int(lib().lora_mlp_launch_count()) + int(lib().lora_step_launch_count())
+
+
+def step_device_status(stream) -> int:
+    v = ctypes.c_int(0)
+    check(lib().lora_step_device_status(stream, ctypes.byref(v)), "lora_step_device_status")
+    return v.value
 
 
 def make_lin_shape(N, d_in, d_out, r, alpha, weight_format=WEIGHTS_BF16) -> LinShape:
@@ -366,3 +404,19 @@ def ce_device_status(stream) -> int:
     st = ctypes.c_int(0)
     check(lib().lora_ce_device_status(stream, ctypes.byref(st)), "lora_ce_device_status")
     return st.value
+
+
+def embedding_forward(N, V, d, scale, ids, E, out, stream) -> int:
+    return lib().lora_embedding_forward(int(N), int(V), int(d), float(scale), ids, E, out, stream)
+
+
+def embedding_sizes(N, V, d) -> int:
+    ws = ctypes.c_size_t()
+    check(lib().lora_embedding_sizes(int(N), int(V), int(d), ctypes.byref(ws)), "lora_embedding_sizes")
+    return ws.value
+
+
+def embedding_backward(N, V, d, scale, padding_idx, grad_type, ids, dOut, dE, workspace, workspace_bytes,
+                       stream) -> int:
+    return lib().lora_embedding_backward(int(N), int(V), int(d), float(scale), int(padding_idx), int(grad_type), ids,
+                                         dOut, dE, workspace, workspace_bytes, stream)

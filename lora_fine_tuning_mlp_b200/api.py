@@ -741,3 +741,68 @@ class CrossEntropyFunction(torch.autograd.Function):
         if inplace:
             torch.autograd.graph.increment_version(logits)
         return dz, None, None, None, None, None
+
+
+# ----------------------------------------------------------------------------- token embedding
+
+
+def embedding_forward(ids: torch.Tensor, E: torch.Tensor, *, scale: float = 1.0, out=None, stream=None):
+    """out [N, d] = scale * E[ids] (bf16, rounded once) for int64 ids [N] and a bf16 table E [V, d], d a multiple
+    of 8.  The row of an id outside [0, V) is NaN, and step_device_status reports it."""
+    _need(ids, "ids", torch.int64)
+    _need(E, "E", BF16)
+    if ids.dim() != 1 or E.dim() != 2:
+        raise ValueError("ids must be [N] and E [V, d]")
+    (N,), (V, d) = ids.shape, E.shape
+    out = torch.empty((N, d), dtype=BF16, device=E.device) if out is None else _need(out, "out", BF16, (N, d))
+    _lib.check(_lib.embedding_forward(N, V, d, scale, _p(ids), _p(E), _p(out), _stream(stream)),
+               "lora_embedding_forward")
+    return out
+
+
+def embedding_backward(dOut: torch.Tensor, ids: torch.Tensor, V: int, *, scale: float = 1.0, padding_idx=None,
+                       dtype=BF16, dE=None, workspace: Workspace | None = None, stream=None):
+    """dE [V, d], the gradient of embedding_forward's table: each row the sum of its tokens' rows of dOut [N, d]
+    (in fp32, in a fixed order), rounded once to `dtype` (bf16 or fp32); zeros for ids without a token and for
+    padding_idx."""
+    _need(dOut, "dOut", BF16)
+    if dOut.dim() != 2:
+        raise ValueError("dOut must be [N, d]")
+    N, d = dOut.shape
+    _need(ids, "ids", torch.int64, (N,))
+    kind = {BF16: _lib.EMBEDDING_GRAD_BF16, torch.float32: _lib.EMBEDDING_GRAD_FP32}.get(dtype)
+    if kind is None:
+        raise TypeError("dtype must be torch.bfloat16 or torch.float32")
+    if padding_idx is not None and not 0 <= padding_idx < V:
+        raise ValueError(f"padding_idx must be in [0, {V})")
+    dev = dOut.device
+    dE = torch.empty((V, d), dtype=dtype, device=dev) if dE is None else _need(dE, "dE", dtype, (V, d))
+    ws = (workspace or Workspace()).get(_lib.embedding_sizes(N, V, d), dev)
+    _lib.check(_lib.embedding_backward(N, V, d, scale, -1 if padding_idx is None else padding_idx, kind, _p(ids),
+                                       _p(dOut), _p(dE), _p(ws), ws.numel(), _stream(stream)),
+               "lora_embedding_backward")
+    return dE
+
+
+class EmbeddingFunction(torch.autograd.Function):
+    """autograd wrapper of the scaled lookup: out = scale * E[ids].  Usage:
+    EmbeddingFunction.apply(ids, E, scale, padding_idx) (padding_idx None or an id whose row gets no gradient)."""
+
+    @staticmethod
+    def forward(ctx, ids, E, scale=1.0, padding_idx=None):
+        ids = ids.contiguous()
+        ctx.save_for_backward(ids)
+        ctx.cfg = (E.shape[0], scale, padding_idx)
+        return embedding_forward(ids, E, scale=scale)
+
+    @staticmethod
+    def backward(ctx, dOut):
+        (ids,) = ctx.saved_tensors
+        V, scale, padding_idx = ctx.cfg
+        return None, embedding_backward(dOut.contiguous(), ids, V, scale=scale, padding_idx=padding_idx), None, None
+
+
+def step_device_status(stream=None) -> int:
+    """Reads and clears the device-side status of the operators around the dense layers (embedding): 0, or
+    _lib.ERR_INVALID_ARG after an id outside its range.  Synchronises the stream."""
+    return _lib.step_device_status(_stream(stream))

@@ -1,0 +1,38 @@
+// Eight bf16 values as one 16-byte vector, widened to fp32 and rounded back.
+#pragma once
+#include <cuda_bf16.h>
+#include <cstdint>
+
+namespace lmlp {
+namespace step {
+
+__device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 round8(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 16 bytes that this launch reads once.
+__device__ __forceinline__ uint4 load_once(const void* p) { return __ldcs(static_cast<const uint4*>(p)); }
+
+// The kernel before this one in the stream has ended and its writes are
+// visible (programmatic dependent launch; nothing to wait for otherwise).
+__device__ __forceinline__ void wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel in the stream may start its blocks.
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+}  // namespace step
+}  // namespace lmlp
