@@ -1,5 +1,5 @@
 """ctypes binding of liblora_mlp.so (include/lora_mlp.h, lora_linear.h, lora_rmsnorm.h, lora_ce.h; lora_step.h,
-lora_embedding.h).
+lora_embedding.h, lora_qk_rope.h, lora_distill.h).
 
 Argument marshalling only: every step of the MLP runs in the library's CUDA
 kernels.  Loading fails loudly if the shared library has not been built.
@@ -67,7 +67,8 @@ SYMBOLS = (
     "lora_ce_device_status",
 )
 
-# Every symbol of the operators around the dense layers: lora_step.h and lora_embedding.h.
+# Every symbol of the operators around the dense layers: lora_step.h, lora_embedding.h, lora_qk_rope.h and
+# lora_distill.h.
 STEP_SYMBOLS = (
     "lora_step_device_status",
     "lora_step_timing_enable",
@@ -76,10 +77,25 @@ STEP_SYMBOLS = (
     "lora_embedding_forward",
     "lora_embedding_sizes",
     "lora_embedding_backward",
+    "lora_qk_rope_forward",
+    "lora_qk_rope_sizes",
+    "lora_qk_rope_backward",
+    "lora_distill_forward",
+    "lora_distill_backward",
+    "lora_distill_backward_reduced",
+    "lora_distill_sizes",
+    "lora_distill_loss",
 )
 
 EMBEDDING_GRAD_BF16 = 0
 EMBEDDING_GRAD_FP32 = 1
+
+DISTILL_VALUES_BF16 = 0
+DISTILL_VALUES_FP32 = 1
+DISTILL_IDS_INT32 = 0
+DISTILL_IDS_INT64 = 1
+DISTILL_REDUCTION_SUM = 1
+DISTILL_REDUCTION_MEAN = 2
 
 
 class Shape(ctypes.Structure):
@@ -107,6 +123,22 @@ class LinWeights(ctypes.Structure):
 class CEShape(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("V", ctypes.c_int64), ("ld", ctypes.c_int64),
                 ("logit_scale", ctypes.c_float), ("softcap", ctypes.c_float), ("ignore_index", ctypes.c_int64)]
+
+
+class QKShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "S", "Hq", "Hk", "D", "rot", "P", "position_stride")] + [
+        ("eps", ctypes.c_float), ("interleaved", ctypes.c_int32)]
+
+
+class QKView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_s", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
+class DistillShape(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("V", ctypes.c_int64), ("ld", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("temperature", ctypes.c_float), ("logit_scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("values_type", ctypes.c_int32), ("ids_type", ctypes.c_int32), ("ignore_index", ctypes.c_int64)]
 
 
 class KernelTime(ctypes.Structure):
@@ -186,6 +218,15 @@ def lib() -> ctypes.CDLL:
             L.lora_embedding_sizes.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
             L.lora_embedding_backward.argtypes = [i64, i64, i64, ctypes.c_float, i64, ctypes.c_int, vp, vp, vp, vp, sz,
                                                   vp]
+            qs, qv, ds = ctypes.POINTER(QKShape), ctypes.POINTER(QKView), ctypes.POINTER(DistillShape)
+            L.lora_qk_rope_forward.argtypes = [qs, qv, qv, vp, vp, vp, vp, vp, qv, qv, vp]
+            L.lora_qk_rope_sizes.argtypes = [qs, ctypes.POINTER(sz)]
+            L.lora_qk_rope_backward.argtypes = [qs, qv, qv, vp, vp, vp, vp, vp, qv, qv, qv, qv, vp, vp, vp, sz, vp]
+            L.lora_distill_forward.argtypes = [ds, vp, vp, vp, vp, vp, vp]
+            L.lora_distill_backward.argtypes = [ds, vp, vp, vp, vp, vp, vp, vp]
+            L.lora_distill_backward_reduced.argtypes = [ds, vp, vp, vp, vp, vp, vp, vp, vp]
+            L.lora_distill_sizes.argtypes = [ds, ctypes.POINTER(sz)]
+            L.lora_distill_loss.argtypes = [ds, vp, vp, vp, vp, ctypes.c_int, vp, vp, vp, sz, vp]
             for name in STEP_SYMBOLS:
                 getattr(L, name).restype = ctypes.c_int
             L.lora_step_launch_count.restype = ctypes.c_int64
@@ -420,3 +461,47 @@ def embedding_backward(N, V, d, scale, padding_idx, grad_type, ids, dOut, dE, wo
                        stream) -> int:
     return lib().lora_embedding_backward(int(N), int(V), int(d), float(scale), int(padding_idx), int(grad_type), ids,
                                          dOut, dE, workspace, workspace_bytes, stream)
+
+
+def qk_rope_forward(shape: QKShape, q, k, q_gain, k_gain, cos, sin, positions, q_out, k_out, stream) -> int:
+    """q, k, q_out, k_out: QKView."""
+    return lib().lora_qk_rope_forward(shape, q, k, q_gain, k_gain, cos, sin, positions, q_out, k_out, stream)
+
+
+def qk_rope_sizes(shape: QKShape) -> int:
+    ws = ctypes.c_size_t()
+    check(lib().lora_qk_rope_sizes(ctypes.byref(shape), ctypes.byref(ws)), "lora_qk_rope_sizes")
+    return ws.value
+
+
+def qk_rope_backward(shape: QKShape, q, k, q_gain, k_gain, cos, sin, positions, dq_out, dk_out, dq, dk, dq_gain,
+                     dk_gain, workspace, workspace_bytes, stream) -> int:
+    """q, k, dq_out, dk_out, dq, dk: QKView (q, k may be None without gains)."""
+    return lib().lora_qk_rope_backward(shape, q, k, q_gain, k_gain, cos, sin, positions, dq_out, dk_out, dq, dk,
+                                       dq_gain, dk_gain, workspace, workspace_bytes, stream)
+
+
+def distill_forward(shape: DistillShape, logits, values, ids, labels, loss, stream) -> int:
+    return lib().lora_distill_forward(ctypes.byref(shape), logits, values, ids, labels, loss, stream)
+
+
+def distill_backward(shape: DistillShape, logits, values, ids, labels, dloss, dlogits, stream) -> int:
+    return lib().lora_distill_backward(ctypes.byref(shape), logits, values, ids, labels, dloss, dlogits, stream)
+
+
+def distill_backward_reduced(shape: DistillShape, logits, values, ids, labels, dout, fwd_out, dlogits,
+                             stream) -> int:
+    return lib().lora_distill_backward_reduced(ctypes.byref(shape), logits, values, ids, labels, dout, fwd_out,
+                                               dlogits, stream)
+
+
+def distill_sizes(shape: DistillShape) -> int:
+    ws = ctypes.c_size_t()
+    check(lib().lora_distill_sizes(ctypes.byref(shape), ctypes.byref(ws)), "lora_distill_sizes")
+    return ws.value
+
+
+def distill_loss(shape: DistillShape, logits, values, ids, labels, reduction, out, dlogits, workspace,
+                 workspace_bytes, stream) -> int:
+    return lib().lora_distill_loss(ctypes.byref(shape), logits, values, ids, labels, int(reduction), out, dlogits,
+                                   workspace, workspace_bytes, stream)

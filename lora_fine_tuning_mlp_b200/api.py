@@ -802,7 +802,285 @@ class EmbeddingFunction(torch.autograd.Function):
         return None, embedding_backward(dOut.contiguous(), ids, V, scale=scale, padding_idx=padding_idx), None, None
 
 
+# ----------------------------------------------------------------------------- queries' and keys' norm and rotation
+
+
+def rope_table(P: int, rot: int, *, base: float = 10000.0, device=None):
+    """(cos, sin), fp32 [P, rot/2], of the plain rotation: pair i of position p turns by p * base^(-2i/rot).  The
+    angles are formed in fp64, so that far positions keep theirs.  A program makes the table once; one with scaled
+    frequencies fills its own."""
+    if P < 1 or rot < 2 or rot % 2:
+        raise ValueError("P must be at least 1 and rot even")
+    freq = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    angle = torch.arange(P, dtype=torch.float64, device=device)[:, None] * freq
+    return angle.cos().float(), angle.sin().float()
+
+
+def _heads(t, name, shape=None, written=False):
+    """A [B, S, heads, D] (or [S, heads, D]) view for the library; the last axis contiguous, other strides multiples
+    of 8.  Returns (QKView, its four sizes)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != BF16:
+        raise TypeError(f"{name} must be {BF16}, got {t.dtype}")
+    n = t.shape
+    if len(n) not in (3, 4) or (shape is not None and tuple(n) != tuple(shape)):
+        raise ValueError(f"{name} has shape {tuple(n)}, expected " +
+                         ("[B, S, heads, D] or [S, heads, D]" if shape is None else str(tuple(shape))))
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"the elements of a head of {name} must be contiguous")
+    # the stride of an axis of one entry is never used, and may be anything
+    v = [st[i] if n[i] > 1 else 0 for i in range(-len(n), -1)]
+    if any(x % 8 for x in v):
+        raise ValueError(f"the strides of {name} must be multiples of 8")
+    if written and any(x == 0 and n[i] > 1 for i, x in enumerate(v)):
+        raise ValueError(f"{name} must not overlap itself")
+    if len(n) == 3:
+        return _lib.QKView(t.data_ptr(), 0, *v), (1, *n)
+    return _lib.QKView(t.data_ptr(), *v), tuple(n)
+
+
+def _qk_call(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved):
+    """Checked arguments of both passes: (shape, view of q, view of k, gains, cos, sin, positions as pointers)."""
+    vq, (B, S, Hq, D) = _heads(q, "q")
+    vk, (Bk, Sk, Hk, Dk) = _heads(k, "k")
+    if (B, S, D) != (Bk, Sk, Dk) or q.dim() != k.dim():
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} differ in more than their heads")
+    _need(cos, "cos", torch.float32)
+    if cos.dim() != 2:
+        raise ValueError("cos must be [P, rot/2]")
+    _need(sin, "sin", torch.float32, cos.shape)
+    if (q_gain is None) != (k_gain is None):
+        raise ValueError("q_gain and k_gain are given together or not at all")
+    if q_gain is not None:
+        _need(q_gain, "q_gain", BF16, (D,))
+        _need(k_gain, "k_gain", BF16, (D,))
+    stride = 0
+    if positions is not None:
+        _need(positions, "positions", torch.int64)
+        if tuple(positions.shape) == (B, S):
+            stride = S
+        elif tuple(positions.shape) != (S,):
+            raise ValueError(f"positions must be [{S}] or [{B}, {S}], got {list(positions.shape)}")
+    shape = _lib.QKShape(B, S, Hq, Hk, D, 2 * cos.shape[1], cos.shape[0], stride, eps, 1 if interleaved else 0)
+    return shape, vq, vk, (_p(q_gain), _p(k_gain), _p(cos), _p(sin), _p(positions))
+
+
+def qk_norm_rope_forward(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, *, positions=None,
+                         q_gain=None, k_gain=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
+                         k_out=None, stream=None):
+    """(q_out, k_out): each head of q [B, S, Hq, D] and k [B, S, Hk, D] (or without B) normed (times q_gain, k_gain
+    [D]; no norm without them) and turned by its position's angles, cos and sin fp32 [P, rot/2].  positions: int64
+    [B, S] or [S], else 0 .. S-1.  Pairs are (i, i + rot/2), or (2i, 2i + 1) with interleaved; elements from rot on
+    do not turn.  q, k and given outputs may be strided views; new outputs are contiguous."""
+    shape, vq, vk, rest = _qk_call(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved)
+    q_out = torch.empty(q.shape, dtype=BF16, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=BF16, device=k.device) if k_out is None else k_out
+    _lib.check(_lib.qk_rope_forward(shape, vq, vk, *rest, _heads(q_out, "q_out", q.shape, True)[0],
+                                    _heads(k_out, "k_out", k.shape, True)[0], _stream(stream)),
+               "lora_qk_rope_forward")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor,
+                          dq_out: torch.Tensor, dk_out: torch.Tensor, *, positions=None, q_gain=None, k_gain=None,
+                          eps: float = 1e-6, interleaved: bool = False, gain_grads: bool = True, dq=None, dk=None,
+                          workspace: Workspace | None = None, stream=None):
+    """(dq, dk, dq_gain, dk_gain) from the forward's arguments and the gradients of its results; the gains'
+    gradients are fp32 [D], None without gains or with gain_grads=False (frozen gains)."""
+    shape, vq, vk, rest = _qk_call(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved)
+    dev = q.device
+    dq = torch.empty(q.shape, dtype=BF16, device=dev) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=BF16, device=dev) if dk is None else dk
+    dgq = dgk = ws = None
+    if q_gain is not None and gain_grads:
+        dgq, dgk = torch.empty((2, shape.D), dtype=torch.float32, device=dev).unbind(0)
+        ws = (workspace or Workspace()).get(_lib.qk_rope_sizes(shape), dev)
+    _lib.check(_lib.qk_rope_backward(shape, vq, vk, *rest, _heads(dq_out, "dq_out", q.shape)[0],
+                                     _heads(dk_out, "dk_out", k.shape)[0], _heads(dq, "dq", q.shape, True)[0],
+                                     _heads(dk, "dk", k.shape, True)[0], _p(dgq), _p(dgk), _p(ws),
+                                     0 if ws is None else ws.numel(), _stream(stream)), "lora_qk_rope_backward")
+    return dq, dk, dgq, dgk
+
+
+def _heads_or_copy(t):
+    """t itself where the library takes its strides, else a contiguous copy (autograd hands over any)."""
+    ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(s % 8 == 0 for s in t.stride()[:-1])
+    return t if ok else t.contiguous()
+
+
+class QKNormRopeFunction(torch.autograd.Function):
+    """autograd wrapper of the norm and rotation of queries and keys.  Usage:
+    QKNormRopeFunction.apply(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved) -> (q_out, k_out);
+    the gains may be None, and get a gradient where they require one."""
+
+    @staticmethod
+    def forward(ctx, q, k, cos, sin, positions=None, q_gain=None, k_gain=None, eps=1e-6, interleaved=False):
+        q, k = _heads_or_copy(q), _heads_or_copy(k)
+        ctx.save_for_backward(q, k, cos, sin, positions, q_gain, k_gain)
+        ctx.cfg = (eps, interleaved)
+        return qk_norm_rope_forward(q, k, cos, sin, positions=positions, q_gain=q_gain, k_gain=k_gain, eps=eps,
+                                    interleaved=interleaved)
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, cos, sin, positions, q_gain, k_gain = ctx.saved_tensors
+        eps, interleaved = ctx.cfg
+        want = q_gain is not None and (ctx.needs_input_grad[5] or ctx.needs_input_grad[6])
+        dq, dk, dgq, dgk = qk_norm_rope_backward(
+            q, k, cos, sin, _heads_or_copy(dq_out), _heads_or_copy(dk_out), positions=positions, q_gain=q_gain,
+            k_gain=k_gain, eps=eps, interleaved=interleaved, gain_grads=want)
+        if want:
+            dgq, dgk = dgq.to(q_gain.dtype), dgk.to(k_gain.dtype)
+        return dq, dk, None, None, None, dgq, dgk, None, None
+
+
+# ----------------------------------------------------------------------------- distillation
+
+
+def _distill_call(logits, values, ids, labels, temperature, logit_scale, softcap, ignore_index):
+    """Checked arguments of every pass: (shape, logits, values, ids, labels as pointers)."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be [N, V]")
+    if logits.dtype != BF16 or not logits.is_cuda:
+        raise TypeError("logits must be a bf16 CUDA tensor")
+    if logits.stride(1) != 1 and logits.shape[1] > 1:
+        raise ValueError("logits rows must be contiguous")
+    N, V = logits.shape
+    if not isinstance(values, torch.Tensor) or values.dim() != 2:
+        raise ValueError("teacher_logits must be [N, K]")
+    if values.dtype not in (BF16, torch.float32):
+        raise TypeError("teacher_logits must be bf16 or fp32")
+    K = values.shape[1]
+    _need(values, "teacher_logits", values.dtype, (N, K))
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("teacher_ids must be an int32 or int64 tensor")
+    _need(ids, "teacher_ids", ids.dtype, (N, K))
+    if labels is not None:
+        _need(labels, "labels", torch.int64, (N,))
+    ld = logits.stride(0) if N > 1 else (V + 7) // 8 * 8  # one row: its stride is never used
+    shape = _lib.DistillShape(N, V, ld, K, temperature, logit_scale, softcap,
+                              _lib.DISTILL_VALUES_BF16 if values.dtype == BF16 else _lib.DISTILL_VALUES_FP32,
+                              _lib.DISTILL_IDS_INT32 if ids.dtype == torch.int32 else _lib.DISTILL_IDS_INT64,
+                              ignore_index)
+    return shape, (_p(logits), _p(values), _p(ids), _p(labels))
+
+
+def _distill_out(logits, out, inplace):
+    # the gradient is written with the logits' row stride, as in ce_backward
+    if inplace:
+        return logits
+    if out is None:
+        return torch.empty_strided(logits.size(), logits.stride(), dtype=BF16, device=logits.device)
+    if out.shape != logits.shape or out.stride() != logits.stride() or out.dtype != BF16 or not out.is_cuda:
+        raise ValueError("out must have the logits' shape, strides and dtype")
+    return out
+
+
+def distill_forward(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ids: torch.Tensor, *, labels=None,
+                    temperature: float = 1.0, logit_scale: float = 1.0, softcap: float = 0.0,
+                    ignore_index: int = -100, stream=None):
+    """loss [N] fp32: for each row of the student's bf16 logits [N, V] (row stride a multiple of 8), T^2 times the
+    divergence of the student's softmax from the teacher's, taken over the teacher's K highest logits
+    teacher_logits [N, K] (bf16 or fp32) at teacher_ids [N, K] (int32 or int64, -1: no entry).  0 for rows whose
+    label (int64 [N], optional) is ignore_index and for rows without an entry."""
+    shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
+                                ignore_index)
+    loss = torch.empty((shape.N,), dtype=torch.float32, device=logits.device)
+    _lib.check(_lib.distill_forward(shape, *ptrs, _p(loss), _stream(stream)), "lora_distill_forward")
+    return loss
+
+
+def distill_backward(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ids: torch.Tensor,
+                     dloss: torch.Tensor, *, labels=None, temperature: float = 1.0, logit_scale: float = 1.0,
+                     softcap: float = 0.0, ignore_index: int = -100, out=None, inplace: bool = False, stream=None):
+    """dlogits [N, V] bf16 for the per-row upstream gradient dloss [N] (fp32).  inplace=True writes the gradient
+    over the logits."""
+    shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
+                                ignore_index)
+    _need(dloss, "dloss", torch.float32, (shape.N,))
+    out = _distill_out(logits, out, inplace)
+    _lib.check(_lib.distill_backward(shape, *ptrs, _p(dloss), _p(out), _stream(stream)), "lora_distill_backward")
+    return out
+
+
+def distill_loss(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ids: torch.Tensor, *, labels=None,
+                 reduction: str = "mean", temperature: float = 1.0, logit_scale: float = 1.0, softcap: float = 0.0,
+                 ignore_index: int = -100, with_grad: bool = True, grad_out=None, inplace: bool = False,
+                 workspace: Workspace | None = None, stream=None):
+    """The rows' losses reduced ("mean" over the rows whose label is not ignore_index, or "sum") and, with
+    with_grad, the gradient in the same pass over the logits: returns (out [2] fp32, dlogits or None), out[0] the
+    loss and out[1] its derivative with respect to a row's loss.  dlogits is the gradient of out[0]:
+    logits.backward(dlogits) goes on from there.  inplace=True writes it over the logits."""
+    red = {"sum": _lib.DISTILL_REDUCTION_SUM, "mean": _lib.DISTILL_REDUCTION_MEAN}.get(reduction)
+    if red is None:
+        raise ValueError("reduction must be 'sum' or 'mean'")
+    shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
+                                ignore_index)
+    dev = logits.device
+    out = torch.empty((2,), dtype=torch.float32, device=dev)
+    dlogits = _distill_out(logits, grad_out, inplace) if with_grad else None
+    ws = (workspace or Workspace()).get(_lib.distill_sizes(shape), dev)
+    _lib.check(_lib.distill_loss(shape, *ptrs, red, _p(out), _p(dlogits), _p(ws), ws.numel(), _stream(stream)),
+               "lora_distill_loss")
+    return out, dlogits
+
+
+def distill_backward_reduced(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ids: torch.Tensor,
+                             dout: torch.Tensor, fwd_out: torch.Tensor, *, labels=None, temperature: float = 1.0,
+                             logit_scale: float = 1.0, softcap: float = 0.0, ignore_index: int = -100, out=None,
+                             inplace: bool = False, stream=None):
+    """dlogits [N, V] bf16 for the upstream gradient dout (fp32, one element) of the loss distill_loss returned in
+    fwd_out."""
+    shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
+                                ignore_index)
+    _need(fwd_out, "fwd_out", torch.float32, (2,))
+    if dout.numel() != 1 or dout.dtype != torch.float32 or not dout.is_cuda:
+        raise TypeError("dout must be one fp32 CUDA element")
+    out = _distill_out(logits, out, inplace)
+    _lib.check(_lib.distill_backward_reduced(shape, *ptrs, _p(dout), _p(fwd_out), _p(out), _stream(stream)),
+               "lora_distill_backward_reduced")
+    return out
+
+
+class DistillFunction(torch.autograd.Function):
+    """Mean distillation loss over the rows whose label is not ignore_index.  Usage:
+    DistillFunction.apply(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
+    ignore_index, inplace) (labels may be None).  No gradient for the teacher.  The backward reads the logits again,
+    so that it can apply any upstream gradient before it rounds; a loop whose loss is this one alone saves that
+    reading with distill_loss.  inplace=True writes the gradient over the logits, whose version counter is then
+    bumped, as in CrossEntropyFunction."""
+
+    @staticmethod
+    def forward(ctx, logits, teacher_logits, teacher_ids, labels=None, temperature=1.0, logit_scale=1.0, softcap=0.0,
+                ignore_index=-100, inplace=False):
+        kw = {"temperature": temperature, "logit_scale": logit_scale, "softcap": softcap,
+              "ignore_index": ignore_index}
+        out, _ = distill_loss(logits, teacher_logits, teacher_ids, labels=labels, with_grad=False, **kw)
+        ctx.save_for_backward(logits, teacher_logits, teacher_ids, labels, out)
+        ctx.cfg = (kw, bool(inplace))
+        return out[0]
+
+    @staticmethod
+    def backward(ctx, g):
+        logits, teacher_logits, teacher_ids, labels, out = ctx.saved_tensors
+        kw, inplace = ctx.cfg
+        if g.dtype != torch.float32 or not g.is_cuda:
+            raise TypeError("the upstream gradient of the loss must be fp32 on the GPU")
+        dz = distill_backward_reduced(logits, teacher_logits, teacher_ids, g.contiguous(), out, labels=labels,
+                                      inplace=inplace, **kw)
+        if inplace:
+            torch.autograd.graph.increment_version(logits)
+        return dz, None, None, None, None, None, None, None, None
+
+
+# ----------------------------------------------------------------------------- status
+
+
 def step_device_status(stream=None) -> int:
-    """Reads and clears the device-side status of the operators around the dense layers (embedding): 0, or
-    _lib.ERR_INVALID_ARG after an id outside its range.  Synchronises the stream."""
+    """Reads and clears the device-side status of the operators around the dense layers (embedding, norm and rotation of queries and
+    keys, distillation): 0, or _lib.ERR_INVALID_ARG after an id or position outside its range.  Synchronises the stream."""
     return _lib.step_device_status(_stream(stream))

@@ -1,6 +1,6 @@
 // C ABI of the operators around a fine-tuning step's dense layers
-// (include/lora_step.h, lora_embedding.h): argument checks, workspace layout
-// and launches.
+// (include/lora_step.h, lora_embedding.h, lora_qk_rope.h, lora_distill.h):
+// argument checks, workspace layout and launches.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -11,8 +11,12 @@
 #include <mutex>
 #include <vector>
 
+#include "lora_distill.h"
 #include "lora_embedding.h"
+#include "lora_qk_rope.h"
+#include "distill.cuh"
 #include "embedding.cuh"
+#include "qk_rope.cuh"
 
 using namespace lmlp::step;
 
@@ -77,6 +81,13 @@ int check_args(std::initializer_list<Arg> as) {
     return LORA_MLP_OK;
 }
 
+// Pointers that may be null.
+int check_optional(std::initializer_list<Arg> as) {
+    for (const Arg& a : as)
+        if (reinterpret_cast<uintptr_t>(a.p) % a.align) return LORA_MLP_ERR_MISALIGNED;
+    return LORA_MLP_OK;
+}
+
 // Memory of the current device (after every other check of the arguments).
 int check_memory(std::initializer_list<Arg> as) {
     for (const Arg& a : as)
@@ -125,20 +136,25 @@ struct LaunchScope {
 
 // One launch.  `after_own`: the kernel before it in the stream is one of this
 // call's, which lets it start early and which it waits for itself
-// (programmatic dependent launch).
+// (programmatic dependent launch).  `cluster`: blocks of a thread-block cluster.
 template <class... P, class... A>
-int launch(const char* name, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
-           bool after_own, A... args) {
+int launch(const char* name, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+           bool after_own, int cluster, A... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = after_own ? 1 : 0;
+    cudaLaunchAttribute attr[2] = {};
+    cfg.attrs = attr;
+    if (after_own) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs++].val.clusterDim = {static_cast<unsigned>(cluster), 1u, 1u};
+    }
     LaunchScope scope(name, st);
     if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) != cudaSuccess) {
         cudaGetLastError();
@@ -280,7 +296,7 @@ int lora_embedding_forward(int64_t N, int64_t V, int64_t d, float scale, const i
     a.status = di.status;
     const int rows = kEmbThreads >> a.log_tpr;
     return launch("EMB_fwd", embed_fwd_kernel, dim3(static_cast<unsigned>((N + rows - 1) / rows)), kEmbThreads, 0,
-                  static_cast<cudaStream_t>(stream), false, a);
+                  static_cast<cudaStream_t>(stream), false, 1, a);
 }
 
 int lora_embedding_sizes(int64_t N, int64_t V, int64_t d, size_t* workspace_bytes) {
@@ -323,13 +339,13 @@ int lora_embedding_backward(int64_t N, int64_t V, int64_t d, float scale, int64_
     if (p.small) {
         const size_t smem = sizeof(SortShared) + 2 * sizeof(uint32_t) * kSortSmall;
         STEP_TRY(allow_smem(embed_sort_small_kernel, smem));
-        STEP_TRY(launch("EMB_sort", embed_sort_small_kernel, dim3(1), kSortThreads, smem, st, false, s));
+        STEP_TRY(launch("EMB_sort", embed_sort_small_kernel, dim3(1), kSortThreads, smem, st, false, 1, s));
     } else {
         const dim3 grid(static_cast<unsigned>(p.ntiles));
-        STEP_TRY(launch("EMB_sort_count", embed_sort_count_kernel, grid, kSortThreads, 0, st, false, s));
+        STEP_TRY(launch("EMB_sort_count", embed_sort_count_kernel, grid, kSortThreads, 0, st, false, 1, s));
         for (int i = 0; i < p.passes; ++i)
             STEP_TRY(launch("EMB_sort_scatter", embed_sort_scatter_kernel, grid, kSortThreads, sizeof(SortShared), st,
-                            true, s, i));
+                            true, 1, s, i));
     }
 
     EmbBwdArgs a{};
@@ -356,8 +372,329 @@ int lora_embedding_backward(int64_t N, int64_t V, int64_t d, float scale, int64_
     if (blocks > INT32_MAX) return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
     a.first_wave = static_cast<int>(std::min<int64_t>(nrow, int64_t{kEmbBlocksPerSm} * di.sms));
     const dim3 grid(static_cast<unsigned>(blocks));
-    if (f32) return launch("EMB_grad", embed_bwd_kernel<true>, grid, kEmbThreads, 0, st, true, a);
-    return launch("EMB_grad", embed_bwd_kernel<false>, grid, kEmbThreads, 0, st, true, a);
+    if (f32) return launch("EMB_grad", embed_bwd_kernel<true>, grid, kEmbThreads, 0, st, true, 1, a);
+    return launch("EMB_grad", embed_bwd_kernel<false>, grid, kEmbThreads, 0, st, true, 1, a);
+}
+
+}  // extern "C"
+
+// ============================================================================= queries' and keys' norm and rotation
+
+namespace {
+
+int validate_qk(const lora_qk_shape* sh) {
+    if (sh == nullptr) return LORA_MLP_ERR_INVALID_ARG;
+    if (sh->B < 1 || sh->S < 1 || sh->Hq < 1 || sh->Hk < 1 || sh->P < 1 || sh->rot < 1 || sh->rot > sh->D ||
+        sh->position_stride < 0)
+        return LORA_MLP_ERR_INVALID_ARG;
+    if (!std::isfinite(sh->eps) || sh->eps < 0.0f) return LORA_MLP_ERR_INVALID_ARG;
+    if (sh->D % 16 || sh->rot % 16 || sh->D > 512) return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
+    const int64_t lim = INT32_MAX;
+    if (sh->B > lim || sh->S > lim || sh->Hq > 65536 || sh->Hk > 65536 || sh->P > lim || sh->B * sh->S > lim)
+        return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
+    return LORA_MLP_OK;
+}
+
+int check_view(const lora_qk_view* v) {
+    if (v == nullptr || v->data == nullptr) return LORA_MLP_ERR_INVALID_ARG;
+    if (v->stride_b % 8 || v->stride_s % 8 || v->stride_h % 8) return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
+    return reinterpret_cast<uintptr_t>(v->data) % 16 ? LORA_MLP_ERR_MISALIGNED : LORA_MLP_OK;
+}
+
+QkView qk_view(const lora_qk_view* v) {
+    return {static_cast<uint4*>(v->data), v->stride_b / 8, v->stride_s / 8, v->stride_h / 8};
+}
+
+QkArgs qk_args(const lora_qk_shape* sh, const void* q_gain, const void* k_gain, const float* cos, const float* sin,
+               const int64_t* positions, int* status, int unroll) {
+    QkArgs a{};
+    a.gain[0] = static_cast<const uint4*>(q_gain);
+    a.gain[1] = static_cast<const uint4*>(k_gain);
+    a.cos = cos;
+    a.sin = sin;
+    a.pos = reinterpret_cast<const long long*>(positions);
+    a.pos_stride = sh->position_stride;
+    a.T = sh->B * sh->S;
+    a.S = sh->S;
+    a.P = sh->P;
+    a.H[0] = static_cast<int>(sh->Hq);
+    a.H[1] = static_cast<int>(sh->Hk);
+    a.D = static_cast<int>(sh->D);
+    a.nslot = a.D / 16;
+    a.nrot = static_cast<int>(sh->rot / 16);
+    a.half = static_cast<int>(sh->rot / 2);
+    a.log_group = ceil_log2(static_cast<uint64_t>(a.nslot));
+    a.eps = sh->eps;
+    a.inv_d = 1.0f / static_cast<float>(a.D);
+    a.turn = 1.0f;
+    a.status = status;
+    const int heads = (32 >> a.log_group) * unroll;
+    for (int i = 0; i < 2; ++i) a.units[i] = (a.H[i] + heads - 1) / heads;
+    return a;
+}
+
+// Both passes without the norm, and the forward with it: one unit a warp.
+int launch_qk(const char* name, const QkArgs& a, bool norm, bool inter, cudaStream_t st) {
+    const int64_t units = a.T * (a.units[0] + a.units[1]);
+    const int64_t blocks = (units + kQkWarps - 1) / kQkWarps;
+    if (blocks > INT32_MAX) return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
+    auto kernel = norm ? (inter ? qk_rope_kernel<true, true> : qk_rope_kernel<true, false>)
+                       : (inter ? qk_rope_kernel<false, true> : qk_rope_kernel<false, false>);
+    return launch(name, kernel, dim3(static_cast<unsigned>(blocks)), kQkThreads, 0, st, false, 1, a);
+}
+
+// Blocks of the backward through the norm for queries and keys: together at
+// most kQkBwdBlocks, shared in proportion to their units.
+constexpr int64_t kQkBwdBlocks = 148 * 5;
+
+void qk_bwd_blocks(const QkArgs& a, int64_t (&blocks)[2]) {
+    const int64_t uq = a.T * a.units[0], uk = a.T * a.units[1];
+    const int64_t q = std::max<int64_t>(1, kQkBwdBlocks * uq / (uq + uk));
+    blocks[0] = std::min((uq + kQkWarps - 1) / kQkWarps, std::min(q, kQkBwdBlocks - 1));
+    blocks[1] = std::min((uk + kQkWarps - 1) / kQkWarps, std::max<int64_t>(1, kQkBwdBlocks - q));
+}
+
+}  // namespace
+
+extern "C" {
+
+int lora_qk_rope_forward(const lora_qk_shape* shape, const lora_qk_view* q, const lora_qk_view* k,
+                         const void* q_gain, const void* k_gain, const float* cos, const float* sin,
+                         const int64_t* positions, const lora_qk_view* q_out, const lora_qk_view* k_out,
+                         void* stream) {
+    STEP_TRY(validate_qk(shape));
+    if ((q_gain == nullptr) != (k_gain == nullptr)) return LORA_MLP_ERR_INVALID_ARG;
+    if (positions == nullptr && shape->S > shape->P) return LORA_MLP_ERR_INVALID_ARG;
+    for (const lora_qk_view* v : {q, k, q_out, k_out}) STEP_TRY(check_view(v));
+    STEP_TRY(check_args({{cos, 16}, {sin, 16}}));
+    STEP_TRY(check_optional({{q_gain, 16}, {k_gain, 16}, {positions, 8}}));
+    STEP_TRY(check_memory({{q->data, 16}, {k->data, 16}, {q_out->data, 16}, {k_out->data, 16}, {q_gain, 16},
+                           {k_gain, 16}, {cos, 16}, {sin, 16}, {positions, 8}}));
+    DevInfo di;
+    STEP_TRY(device_info(&di));
+    QkArgs a = qk_args(shape, q_gain, k_gain, cos, sin, positions, di.status, kQkUnroll);
+    a.in[0] = qk_view(q);
+    a.in[1] = qk_view(k);
+    a.out[0] = qk_view(q_out);
+    a.out[1] = qk_view(k_out);
+    return launch_qk("QK_rope_fwd", a, q_gain != nullptr, shape->interleaved != 0, static_cast<cudaStream_t>(stream));
+}
+
+int lora_qk_rope_sizes(const lora_qk_shape* shape, size_t* workspace_bytes) {
+    STEP_TRY(validate_qk(shape));
+    if (workspace_bytes) *workspace_bytes = static_cast<size_t>(kQkBwdBlocks) * static_cast<size_t>(shape->D) * 4;
+    return LORA_MLP_OK;
+}
+
+int lora_qk_rope_backward(const lora_qk_shape* shape, const lora_qk_view* q, const lora_qk_view* k,
+                          const void* q_gain, const void* k_gain, const float* cos, const float* sin,
+                          const int64_t* positions, const lora_qk_view* dq_out, const lora_qk_view* dk_out,
+                          const lora_qk_view* dq, const lora_qk_view* dk, float* dq_gain, float* dk_gain,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+    STEP_TRY(validate_qk(shape));
+    const bool norm = q_gain != nullptr, gains = dq_gain != nullptr;
+    if (norm != (k_gain != nullptr) || gains != (dk_gain != nullptr) || (gains && !norm)) return LORA_MLP_ERR_INVALID_ARG;
+    if (positions == nullptr && shape->S > shape->P) return LORA_MLP_ERR_INVALID_ARG;
+    for (const lora_qk_view* v : {dq_out, dk_out, dq, dk}) STEP_TRY(check_view(v));
+    if (norm)
+        for (const lora_qk_view* v : {q, k}) STEP_TRY(check_view(v));
+    STEP_TRY(check_args({{cos, 16}, {sin, 16}}));
+    STEP_TRY(check_optional({{q_gain, 16}, {k_gain, 16}, {positions, 8}, {dq_gain, 4}, {dk_gain, 4}}));
+    if (gains) {
+        STEP_TRY(check_args({{workspace, 16}}));
+        size_t need = 0;
+        STEP_TRY(lora_qk_rope_sizes(shape, &need));
+        if (workspace_bytes < need) return LORA_MLP_ERR_WORKSPACE_TOO_SMALL;
+    }
+    STEP_TRY(check_memory({{norm ? q->data : nullptr, 16}, {norm ? k->data : nullptr, 16}, {dq_out->data, 16},
+                           {dk_out->data, 16}, {dq->data, 16}, {dk->data, 16}, {q_gain, 16}, {k_gain, 16}, {cos, 16},
+                           {sin, 16}, {positions, 8}, {dq_gain, 4}, {dk_gain, 4}, {gains ? workspace : nullptr, 16}}));
+    DevInfo di;
+    STEP_TRY(device_info(&di));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    QkArgs a = qk_args(shape, q_gain, k_gain, cos, sin, positions, di.status, norm ? kQkBwdUnroll : kQkUnroll);
+    a.in[0] = qk_view(dq_out);
+    a.in[1] = qk_view(dk_out);
+    a.out[0] = qk_view(dq);
+    a.out[1] = qk_view(dk);
+    a.turn = -1.0f;
+    if (!norm) return launch_qk("QK_rope_bwd", a, false, shape->interleaved != 0, st);
+    a.x[0] = qk_view(q);
+    a.x[1] = qk_view(k);
+    a.part = gains ? static_cast<float*>(workspace) : nullptr;
+    int64_t blocks[2];
+    qk_bwd_blocks(a, blocks);
+    a.blocks_q = static_cast<int>(blocks[0]);
+    const int all = static_cast<int>(blocks[0] + blocks[1]);
+    STEP_TRY(launch("QK_norm_rope_bwd", shape->interleaved ? qk_rope_bwd_kernel<true> : qk_rope_bwd_kernel<false>,
+                    dim3(static_cast<unsigned>(all)), kQkThreads, 0, st, false, 1, a));
+    if (!gains) return LORA_MLP_OK;
+    return launch("QK_gain_grads", qk_gain_kernel, dim3(static_cast<unsigned>((a.D + 31) / 32), 2), dim3(32, 32), 0, st,
+                  true, 1, static_cast<const float*>(a.part), a.D, a.blocks_q, all, dq_gain, dk_gain);
+}
+
+}  // extern "C"
+
+// ============================================================================= distillation
+
+namespace {
+
+constexpr int64_t kDsMaxV = int64_t{kDsMaxCluster} * 106496;  // 208 KB of shared memory a block
+
+int validate_distill(const lora_distill_shape* sh) {
+    if (sh == nullptr) return LORA_MLP_ERR_INVALID_ARG;
+    if (sh->N < 1 || sh->V < 1 || sh->K < 1 || sh->ld < sh->V) return LORA_MLP_ERR_INVALID_ARG;
+    if (!std::isfinite(sh->temperature) || !(sh->temperature > 0.0f)) return LORA_MLP_ERR_INVALID_ARG;
+    if (!std::isfinite(sh->logit_scale) || sh->logit_scale == 0.0f) return LORA_MLP_ERR_INVALID_ARG;
+    if (!std::isfinite(sh->softcap) || sh->softcap < 0.0f) return LORA_MLP_ERR_INVALID_ARG;
+    if (sh->values_type != LORA_DISTILL_VALUES_BF16 && sh->values_type != LORA_DISTILL_VALUES_FP32)
+        return LORA_MLP_ERR_INVALID_ARG;
+    if (sh->ids_type != LORA_DISTILL_IDS_INT32 && sh->ids_type != LORA_DISTILL_IDS_INT64)
+        return LORA_MLP_ERR_INVALID_ARG;
+    if (sh->ld % 8 || sh->K > kDsMaxK || sh->V > kDsMaxV || sh->N > INT32_MAX / kDsMaxCluster)
+        return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
+    return LORA_MLP_OK;
+}
+
+DsArgs ds_args(const lora_distill_shape* sh, const void* logits, const void* values, const void* ids,
+               const int64_t* labels, int* status) {
+    DsArgs a{};
+    a.z = static_cast<const __nv_bfloat16*>(logits);
+    a.ld = sh->ld;
+    a.V = sh->V;
+    a.N = sh->N;
+    a.K = static_cast<int>(sh->K);
+    a.values = values;
+    a.ids = ids;
+    a.values_f32 = sh->values_type == LORA_DISTILL_VALUES_FP32;
+    a.ids_i64 = sh->ids_type == LORA_DISTILL_IDS_INT64;
+    a.labels = reinterpret_cast<const long long*>(labels);
+    a.ignore = sh->ignore_index;
+    a.T = sh->temperature;
+    a.inv_T = 1.0f / sh->temperature;
+    a.scale = std::fabs(sh->logit_scale);
+    a.flip = sh->logit_scale < 0.0f ? 0x80008000u : 0u;
+    a.cap = sh->softcap;
+    constexpr double kLog2e = 1.4426950408889634;
+    const double kn = (sh->softcap > 0.0f ? 1.0 : std::fabs(static_cast<double>(sh->logit_scale))) / sh->temperature;
+    a.kn = static_cast<float>(kn);
+    a.k = static_cast<float>(kn * kLog2e);
+    if (sh->softcap > 0.0f) a.cap2 = static_cast<float>(2.0 * a.scale / sh->softcap * kLog2e);
+    a.status = status;
+    return a;
+}
+
+// Slices of 64 KB at most (three or four blocks a multiprocessor, so that
+// loads, arithmetic and stores of different rows overlap), larger ones only
+// where eight blocks have no room for the row otherwise; more blocks a row
+// where there are too few rows for the multiprocessors.
+int launch_distill(const char* name, DsArgs a, int sms, cudaStream_t st, bool after_own) {
+    a.log_cluster = 0;
+    const auto slice = [&a](int log_cluster) { return (((a.V + (1 << log_cluster) - 1) >> log_cluster) + 7) / 8 * 8; };
+    while (a.log_cluster < 3 &&
+           (slice(a.log_cluster) > 32768 || ((a.N << a.log_cluster) * 2 <= sms && slice(a.log_cluster) > 4096)))
+        ++a.log_cluster;
+    a.slice = static_cast<int>(slice(a.log_cluster));
+    const int threads = std::min(kDsMaxThreads, std::max(64, a.slice / 8 / 4 / 32 * 32));
+    const size_t smem = static_cast<size_t>(a.slice) * 2 + static_cast<size_t>(a.K) * 12;
+    const bool grad = a.dz != nullptr, cap = a.cap > 0.0f;
+    auto kernel = grad ? (cap ? distill_kernel<true, true> : distill_kernel<true, false>)
+                       : (cap ? distill_kernel<false, true> : distill_kernel<false, false>);
+    STEP_TRY(allow_smem(kernel, kDsMaxV / kDsMaxCluster * 2 + kDsMaxK * 12));
+    return launch(name, kernel, dim3(static_cast<unsigned>(a.N << a.log_cluster)), threads, smem, st, after_own,
+                  1 << a.log_cluster, a);
+}
+
+int check_distill(const lora_distill_shape* sh, const void* logits, const void* values, const void* ids,
+                  const int64_t* labels) {
+    const size_t va = sh->values_type == LORA_DISTILL_VALUES_FP32 ? 4 : 2;
+    const size_t ia = sh->ids_type == LORA_DISTILL_IDS_INT64 ? 8 : 4;
+    STEP_TRY(check_args({{logits, 16}, {values, va}, {ids, ia}}));
+    return check_optional({{labels, 8}});
+}
+
+}  // namespace
+
+extern "C" {
+
+int lora_distill_forward(const lora_distill_shape* shape, const void* logits, const void* values, const void* ids,
+                         const int64_t* labels, float* loss, void* stream) {
+    STEP_TRY(validate_distill(shape));
+    STEP_TRY(check_distill(shape, logits, values, ids, labels));
+    STEP_TRY(check_args({{loss, 4}}));
+    STEP_TRY(check_memory({{logits, 1}, {values, 1}, {ids, 1}, {labels, 1}, {loss, 1}}));
+    DevInfo di;
+    STEP_TRY(device_info(&di));
+    DsArgs a = ds_args(shape, logits, values, ids, labels, di.status);
+    a.loss = loss;
+    return launch_distill("DISTILL_fwd", a, di.sms, static_cast<cudaStream_t>(stream), false);
+}
+
+int lora_distill_backward(const lora_distill_shape* shape, const void* logits, const void* values, const void* ids,
+                          const int64_t* labels, const float* dloss, void* dlogits, void* stream) {
+    STEP_TRY(validate_distill(shape));
+    STEP_TRY(check_distill(shape, logits, values, ids, labels));
+    STEP_TRY(check_args({{dloss, 4}, {dlogits, 16}}));
+    STEP_TRY(check_memory({{logits, 1}, {values, 1}, {ids, 1}, {labels, 1}, {dloss, 1}, {dlogits, 1}}));
+    DevInfo di;
+    STEP_TRY(device_info(&di));
+    DsArgs a = ds_args(shape, logits, values, ids, labels, di.status);
+    a.dloss = dloss;
+    a.dloss_stride = 1;
+    a.dz = static_cast<__nv_bfloat16*>(dlogits);
+    return launch_distill("DISTILL_bwd", a, di.sms, static_cast<cudaStream_t>(stream), false);
+}
+
+int lora_distill_backward_reduced(const lora_distill_shape* shape, const void* logits, const void* values,
+                                  const void* ids, const int64_t* labels, const float* dout, const float* fwd_out,
+                                  void* dlogits, void* stream) {
+    STEP_TRY(validate_distill(shape));
+    STEP_TRY(check_distill(shape, logits, values, ids, labels));
+    STEP_TRY(check_args({{dout, 4}, {fwd_out, 8}, {dlogits, 16}}));
+    STEP_TRY(check_memory({{logits, 1}, {values, 1}, {ids, 1}, {labels, 1}, {dout, 1}, {fwd_out, 1}, {dlogits, 1}}));
+    DevInfo di;
+    STEP_TRY(device_info(&di));
+    DsArgs a = ds_args(shape, logits, values, ids, labels, di.status);
+    a.dloss = dout;
+    a.factor = fwd_out;
+    a.dz = static_cast<__nv_bfloat16*>(dlogits);
+    return launch_distill("DISTILL_bwd", a, di.sms, static_cast<cudaStream_t>(stream), false);
+}
+
+int lora_distill_sizes(const lora_distill_shape* shape, size_t* workspace_bytes) {
+    STEP_TRY(validate_distill(shape));
+    Carver c;
+    c.take(static_cast<size_t>(shape->N) * 4);
+    if (workspace_bytes) *workspace_bytes = c.off;
+    return LORA_MLP_OK;
+}
+
+int lora_distill_loss(const lora_distill_shape* shape, const void* logits, const void* values, const void* ids,
+                      const int64_t* labels, int reduction, float* out, void* dlogits, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    STEP_TRY(validate_distill(shape));
+    if (reduction != LORA_DISTILL_REDUCTION_SUM && reduction != LORA_DISTILL_REDUCTION_MEAN)
+        return LORA_MLP_ERR_INVALID_ARG;
+    STEP_TRY(check_distill(shape, logits, values, ids, labels));
+    STEP_TRY(check_args({{out, 8}, {workspace, 16}}));
+    STEP_TRY(check_optional({{dlogits, 16}}));
+    size_t need = 0;
+    STEP_TRY(lora_distill_sizes(shape, &need));
+    if (workspace_bytes < need) return LORA_MLP_ERR_WORKSPACE_TOO_SMALL;
+    STEP_TRY(check_memory({{logits, 1}, {values, 1}, {ids, 1}, {labels, 1}, {out, 1}, {dlogits, 1}, {workspace, 1}}));
+    DevInfo di;
+    STEP_TRY(device_info(&di));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool mean = reduction == LORA_DISTILL_REDUCTION_MEAN;
+    DsArgs a = ds_args(shape, logits, values, ids, labels, di.status);
+    STEP_TRY(launch("DISTILL_count", distill_count_kernel, dim3(1), kDsReduceThreads, 0, st, false, 1, a.labels, a.N,
+                    a.ignore, mean, out));
+    a.loss = static_cast<float*>(workspace);
+    a.dz = static_cast<__nv_bfloat16*>(dlogits);
+    a.factor = out;
+    STEP_TRY(launch_distill(dlogits != nullptr ? "DISTILL_loss_grad" : "DISTILL_fwd", a, di.sms, st, true));
+    return launch("DISTILL_reduce", distill_reduce_kernel, dim3(1), kDsReduceThreads, 0, st, true, 1,
+                  static_cast<const float*>(a.loss), a.N, a.labels, a.ignore, mean, out);
 }
 
 }  // extern "C"

@@ -21,3 +21,5 @@ from . import lora_linear  # noqa: F401,E402
 from . import rmsnorm  # noqa: F401,E402
 from . import cross_entropy  # noqa: F401,E402
 from . import embedding  # noqa: F401,E402
+from . import qk_rope  # noqa: F401,E402
+from . import distill  # noqa: F401,E402

@@ -30,7 +30,7 @@ def bf16(rng, *shape, std=1.0):
 
 
 def f64(t):
-    return t.double().cpu().numpy()
+    return t.detach().double().cpu().numpy()
 
 
 @pytest.mark.parametrize("N,V,d,scale", [
