@@ -6,7 +6,6 @@ if the CUDA library is missing or the device is not a B200 the call raises.
 """
 from __future__ import annotations
 
-import ctypes
 from dataclasses import dataclass
 
 import torch
@@ -17,15 +16,19 @@ BF16 = torch.bfloat16
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The address of a stream, by default of the current device's current one (as torch.cuda.current_stream() has
+    it, without the Stream object, which costs 3 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
 def _need(t, name, dtype, shape=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -754,7 +757,7 @@ def embedding_forward(ids: torch.Tensor, E: torch.Tensor, *, scale: float = 1.0,
     if ids.dim() != 1 or E.dim() != 2:
         raise ValueError("ids must be [N] and E [V, d]")
     (N,), (V, d) = ids.shape, E.shape
-    out = torch.empty((N, d), dtype=BF16, device=E.device) if out is None else _need(out, "out", BF16, (N, d))
+    out = E.new_empty((N, d)) if out is None else _need(out, "out", BF16, (N, d))
     _lib.check(_lib.embedding_forward(N, V, d, scale, _p(ids), _p(E), _p(out), _stream(stream)),
                "lora_embedding_forward")
     return out
@@ -817,8 +820,8 @@ def rope_table(P: int, rot: int, *, base: float = 10000.0, device=None):
 
 
 def _heads(t, name, shape=None, written=False):
-    """A [B, S, heads, D] (or [S, heads, D]) view for the library; the last axis contiguous, other strides multiples
-    of 8.  Returns (QKView, its four sizes)."""
+    """A [B, S, heads, D] (or [S, heads, D]) view for the library: the last axis contiguous, other strides multiples
+    of 8."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -826,33 +829,53 @@ def _heads(t, name, shape=None, written=False):
     if t.dtype != BF16:
         raise TypeError(f"{name} must be {BF16}, got {t.dtype}")
     n = t.shape
-    if len(n) not in (3, 4) or (shape is not None and tuple(n) != tuple(shape)):
+    if (len(n) != 4 and len(n) != 3) or (shape is not None and n != shape):
         raise ValueError(f"{name} has shape {tuple(n)}, expected " +
                          ("[B, S, heads, D] or [S, heads, D]" if shape is None else str(tuple(shape))))
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"the elements of a head of {name} must be contiguous")
     # the stride of an axis of one entry is never used, and may be anything
-    v = [st[i] if n[i] > 1 else 0 for i in range(-len(n), -1)]
-    if any(x % 8 for x in v):
+    if len(n) == 4:
+        B, S, H, _ = n
+        sb, ss, sh, se = t.stride()
+    else:
+        B, (S, H, _) = 1, n
+        sb, (ss, sh, se) = 0, t.stride()
+    if B == 1:
+        sb = 0
+    if S == 1:
+        ss = 0
+    if H == 1:
+        sh = 0
+    if se != 1:
+        raise ValueError(f"the elements of a head of {name} must be contiguous")
+    if (sb | ss | sh) & 7:
         raise ValueError(f"the strides of {name} must be multiples of 8")
-    if written and any(x == 0 and n[i] > 1 for i, x in enumerate(v)):
+    if written and ((sb == 0 and B > 1) or (ss == 0 and S > 1) or (sh == 0 and H > 1)):
         raise ValueError(f"{name} must not overlap itself")
-    if len(n) == 3:
-        return _lib.QKView(t.data_ptr(), 0, *v), (1, *n)
-    return _lib.QKView(t.data_ptr(), *v), tuple(n)
+    return _lib.QKView(t.data_ptr(), sb, ss, sh)
+
+
+def _heads_out(t, name, like):
+    """(t or a new contiguous tensor of `like`'s shape, its view)."""
+    if t is not None:
+        return t, _heads(t, name, like.shape, True)
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    S, H, D = t.shape[-3:]
+    return t, _lib.QKView(t.data_ptr(), S * H * D, H * D, D)
 
 
 def _qk_call(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved):
     """Checked arguments of both passes: (shape, view of q, view of k, gains, cos, sin, positions as pointers)."""
-    vq, (B, S, Hq, D) = _heads(q, "q")
-    vk, (Bk, Sk, Hk, Dk) = _heads(k, "k")
-    if (B, S, D) != (Bk, Sk, Dk) or q.dim() != k.dim():
+    vq, vk = _heads(q, "q"), _heads(k, "k")
+    *first, Hq, D = q.shape
+    *others, Hk, Dk = k.shape
+    if first != others or D != Dk:
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} differ in more than their heads")
+    B, S = first if len(first) == 2 else (1, *first)
     _need(cos, "cos", torch.float32)
     if cos.dim() != 2:
         raise ValueError("cos must be [P, rot/2]")
-    _need(sin, "sin", torch.float32, cos.shape)
+    P, half = cos.shape
+    _need(sin, "sin", torch.float32, (P, half))
     if (q_gain is None) != (k_gain is None):
         raise ValueError("q_gain and k_gain are given together or not at all")
     if q_gain is not None:
@@ -861,12 +884,12 @@ def _qk_call(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved):
     stride = 0
     if positions is not None:
         _need(positions, "positions", torch.int64)
-        if tuple(positions.shape) == (B, S):
+        if positions.shape == (B, S):
             stride = S
-        elif tuple(positions.shape) != (S,):
+        elif positions.shape != (S,):
             raise ValueError(f"positions must be [{S}] or [{B}, {S}], got {list(positions.shape)}")
-    shape = _lib.QKShape(B, S, Hq, Hk, D, 2 * cos.shape[1], cos.shape[0], stride, eps, 1 if interleaved else 0)
-    return shape, vq, vk, (_p(q_gain), _p(k_gain), _p(cos), _p(sin), _p(positions))
+    shape = _lib.QKShape(B, S, Hq, Hk, D, 2 * half, P, stride, eps, 1 if interleaved else 0)
+    return shape, vq, vk, (_p(q_gain), _p(k_gain), cos.data_ptr(), sin.data_ptr(), _p(positions))
 
 
 def qk_norm_rope_forward(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, *, positions=None,
@@ -877,11 +900,9 @@ def qk_norm_rope_forward(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, si
     [B, S] or [S], else 0 .. S-1.  Pairs are (i, i + rot/2), or (2i, 2i + 1) with interleaved; elements from rot on
     do not turn.  q, k and given outputs may be strided views; new outputs are contiguous."""
     shape, vq, vk, rest = _qk_call(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved)
-    q_out = torch.empty(q.shape, dtype=BF16, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=BF16, device=k.device) if k_out is None else k_out
-    _lib.check(_lib.qk_rope_forward(shape, vq, vk, *rest, _heads(q_out, "q_out", q.shape, True)[0],
-                                    _heads(k_out, "k_out", k.shape, True)[0], _stream(stream)),
-               "lora_qk_rope_forward")
+    q_out, oq = _heads_out(q_out, "q_out", q)
+    k_out, ok = _heads_out(k_out, "k_out", k)
+    _lib.check(_lib.qk_rope_forward(shape, vq, vk, *rest, oq, ok, _stream(stream)), "lora_qk_rope_forward")
     return q_out, k_out
 
 
@@ -892,16 +913,14 @@ def qk_norm_rope_backward(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, s
     """(dq, dk, dq_gain, dk_gain) from the forward's arguments and the gradients of its results; the gains'
     gradients are fp32 [D], None without gains or with gain_grads=False (frozen gains)."""
     shape, vq, vk, rest = _qk_call(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved)
-    dev = q.device
-    dq = torch.empty(q.shape, dtype=BF16, device=dev) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=BF16, device=dev) if dk is None else dk
+    vdq_out, vdk_out = _heads(dq_out, "dq_out", q.shape), _heads(dk_out, "dk_out", k.shape)
+    dq, vdq = _heads_out(dq, "dq", q)
+    dk, vdk = _heads_out(dk, "dk", k)
     dgq = dgk = ws = None
     if q_gain is not None and gain_grads:
-        dgq, dgk = torch.empty((2, shape.D), dtype=torch.float32, device=dev).unbind(0)
-        ws = (workspace or Workspace()).get(_lib.qk_rope_sizes(shape), dev)
-    _lib.check(_lib.qk_rope_backward(shape, vq, vk, *rest, _heads(dq_out, "dq_out", q.shape)[0],
-                                     _heads(dk_out, "dk_out", k.shape)[0], _heads(dq, "dq", q.shape, True)[0],
-                                     _heads(dk, "dk", k.shape, True)[0], _p(dgq), _p(dgk), _p(ws),
+        dgq, dgk = q.new_empty((2, shape.D), dtype=torch.float32).unbind(0)
+        ws = (workspace or Workspace()).get(_lib.qk_rope_sizes(shape), q.device)
+    _lib.check(_lib.qk_rope_backward(shape, vq, vk, *rest, vdq_out, vdk_out, vdq, vdk, _p(dgq), _p(dgk), _p(ws),
                                      0 if ws is None else ws.numel(), _stream(stream)), "lora_qk_rope_backward")
     return dq, dk, dgq, dgk
 
@@ -974,7 +993,7 @@ def _distill_out(logits, out, inplace):
     if inplace:
         return logits
     if out is None:
-        return torch.empty_strided(logits.size(), logits.stride(), dtype=BF16, device=logits.device)
+        return logits.new_empty_strided(logits.shape, logits.stride())
     if out.shape != logits.shape or out.stride() != logits.stride() or out.dtype != BF16 or not out.is_cuda:
         raise ValueError("out must have the logits' shape, strides and dtype")
     return out
@@ -989,7 +1008,7 @@ def distill_forward(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_
     label (int64 [N], optional) is ignore_index and for rows without an entry."""
     shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
                                 ignore_index)
-    loss = torch.empty((shape.N,), dtype=torch.float32, device=logits.device)
+    loss = logits.new_empty((shape.N,), dtype=torch.float32)
     _lib.check(_lib.distill_forward(shape, *ptrs, _p(loss), _stream(stream)), "lora_distill_forward")
     return loss
 
@@ -1020,10 +1039,9 @@ def distill_loss(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ids
         raise ValueError("reduction must be 'sum' or 'mean'")
     shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
                                 ignore_index)
-    dev = logits.device
-    out = torch.empty((2,), dtype=torch.float32, device=dev)
+    out = logits.new_empty((2,), dtype=torch.float32)
     dlogits = _distill_out(logits, grad_out, inplace) if with_grad else None
-    ws = (workspace or Workspace()).get(_lib.distill_sizes(shape), dev)
+    ws = (workspace or Workspace()).get(_lib.distill_sizes(shape), logits.device)
     _lib.check(_lib.distill_loss(shape, *ptrs, red, _p(out), _p(dlogits), _p(ws), ws.numel(), _stream(stream)),
                "lora_distill_loss")
     return out, dlogits
