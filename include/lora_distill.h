@@ -80,13 +80,13 @@ int lora_distill_backward_reduced(const lora_distill_shape* shape, const void* l
 #define LORA_DISTILL_REDUCTION_SUM 1
 #define LORA_DISTILL_REDUCTION_MEAN 2 /* over the rows whose label is not ignore_index (over 1 if there is none) */
 
-/* Workspace bytes of lora_distill_loss (the rows' losses).  Host only. */
+/* Workspace bytes of lora_distill_loss (the rows' losses and a counter).  Host only. */
 int lora_distill_sizes(const lora_distill_shape* shape, size_t* workspace_bytes);
 
 /* The reduced loss and, where dlogits is not NULL, its gradient in the same
  * pass over the logits.  out is fp32 [2], 8-byte aligned: out[0] the loss
  * (summed in fp64 in a fixed order), out[1] its derivative with respect to the
- * loss of a row that takes part.  dlogits is the gradient of out[0].  Three
+ * loss of a row that takes part.  dlogits is the gradient of out[0].  Two
  * launches. */
 int lora_distill_loss(const lora_distill_shape* shape, const void* logits, const void* values, const void* ids,
                       const int64_t* labels, int reduction, float* out, void* dlogits, void* workspace,

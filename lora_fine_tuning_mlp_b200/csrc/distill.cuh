@@ -13,9 +13,13 @@
 // a multiprocessor overlap one's loads with another's arithmetic.
 //
 // Every thread copies the 16-byte vectors that it later reads (cp.async), so
-// the loads need no barrier.  Sums are taken of 2^((z - m) k) with the
-// difference formed first: exact next to the maximum, and rows filled with
-// bf16's lowest value or with large logits neither overflow nor vanish.
+// the loads need no barrier, and takes them up in four parts as they arrive.
+// Sums are taken of 2^((z - m) k) with the difference formed first: exact next
+// to the maximum, and rows filled with bf16's lowest value or with large
+// logits neither overflow nor vanish.  With softcapping, t = cap tanh(s z /
+// cap) = cap - 2 cap r with r = 1 / (1 + 2^(cap2 z)): exponents are taken of
+// -r, dt/dz = 4 s r (1 - r) has no cancellation where tanh saturates, and four
+// logits share one reciprocal.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -29,6 +33,9 @@ namespace step {
 constexpr int kDsMaxThreads = 256;
 constexpr int kDsMaxCluster = 8;
 constexpr int kDsMaxK = 1024;
+constexpr int kDsParts = 4;   // of a thread's vectors, waited for one after the other
+constexpr int kDsBatch = 4;   // vectors taken up together
+constexpr int kDsEntryBytes = 16;  // of shared memory for a teacher's entry
 constexpr float kDsLowest = -3.3895313892515355e38f;  // bf16's lowest finite value
 
 struct DsArgs {
@@ -45,10 +52,13 @@ struct DsArgs {
     float inv_T, T;
     float scale, cap;     // s with its sign taken off (see flip), cap or 0
     uint32_t flip;        // 0x80008000 where s is negative: z and dz change sign
-    float k;              // log2(e) / T, times s without softcapping: exponents in base 2 per unit of z (of t)
-    float kn;             // the same per unit, base e
+    float k;              // base-2 exponent of a unit of z: s log2(e) / T; of a unit of -r: 2 cap log2(e) / T
+    float kn;             // the natural exponent of the same
     float cap2;           // 2 s / cap * log2(e)
     float* loss;          // may be null
+    float* out;           // the reduced loss, or null
+    uint32_t* counter;    // rows done, zero before the launch (with out)
+    int mean;
     const float* dloss;   // [N], stride 0 or 1 (null: 1)
     long long dloss_stride;
     const float* factor;  // factor[1] multiplies it (null: 1)
@@ -74,313 +84,369 @@ __device__ __forceinline__ uint32_t ds_rank() {
 __device__ __forceinline__ void ds_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void ds_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// What exponents are taken of: z itself, or t = cap tanh(s z / cap) = cap -
-// 2 cap / (1 + 2^(cap2 z)), whose reciprocal saturates to 0 or 1 where tanh is
-// +-1.
+// What exponents are taken of: z, or -r (see above).  2^(cap2 z) is held to
+// 2^30, where tanh is 1 in fp32 already, so that a product of four
+// denominators stays in range; min keeps a NaN.
+__device__ __forceinline__ float ds_denominator(const DsArgs& a, float z) {
+    float e;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(e) : "f"(a.cap2 * z), "f"(30.0f));
+    return 1.0f + ds_ex2(e);
+}
 template <bool CAP>
-__device__ __forceinline__ float ds_t(const DsArgs& a, float z) {
-    return CAP ? fmaf(ds_rcp(1.0f + ds_ex2(a.cap2 * z)), -2.0f * a.cap, a.cap) : z;
+__device__ __forceinline__ float ds_arg(const DsArgs& a, float z) {
+    return CAP ? -ds_rcp(ds_denominator(a, z)) : z;
+}
+template <bool CAP>
+__device__ __forceinline__ void ds_args8(const DsArgs& a, const uint4& v, float (&x)[8]) {
+    widen8(v, x);
+    if constexpr (CAP) {
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+            float d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = ds_denominator(a, x[h + i]);
+            const float d01 = d[0] * d[1], d23 = d[2] * d[3], r = ds_rcp(d01 * d23);
+            const float n01 = -r * d23, n23 = -r * d01;
+            x[h] = n01 * d[1], x[h + 1] = n01 * d[0], x[h + 2] = n23 * d[3], x[h + 3] = n23 * d[2];
+        }
+    }
 }
 
-// (m, s) := (max, sum of 2^((x - max) k)) of the union of two sets.
-__device__ __forceinline__ void ds_merge(float& m, float& s, float m2, float s2, float k) {
-    const float M = fmaxf(m, m2);
-    s = s * ds_ex2((m - M) * k) + s2 * ds_ex2((m2 - M) * k);
-    m = M;
+__device__ __forceinline__ float ds_warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float ds_warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The vector with its signs as the scale's magnitude wants them.
+__device__ __forceinline__ uint4 ds_signed(const DsArgs& a, uint4 v) {
+    if (a.flip) v = make_uint4(v.x ^ a.flip, v.y ^ a.flip, v.z ^ a.flip, v.w ^ a.flip);
+    return v;
+}
+__device__ __forceinline__ void ds_max(uint32_t& m2, const uint4& v) {
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v.x));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v.y));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v.z));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v.w));
 }
 
 struct DsShared {
-    float2 warp[kDsMaxThreads / 32];
-    float2 all[kDsMaxCluster];  // written by every block of the cluster
-    float red[kDsMaxThreads / 32];
-    int bad;
+    float2 warp[32];            // (max, sum) of each warp
+    float2 all[kDsMaxCluster];  // ... of each block of the cluster, written by all of them
+    float inv_psum;             // teacher: 1 / sum of exp((a - max) / T)
+    int live;                   // it has an entry that counts
+    int last;                   // this block reduces the rows' losses
 };
 
-// Sum over the block, the same bits for every thread.
-__device__ __forceinline__ float ds_block_sum(DsShared& s, float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = s.red[0];
-    for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) v += s.red[w];
-    return v;
-}
-__device__ __forceinline__ float ds_block_max(DsShared& s, float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = s.red[0];
-    for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) v = fmaxf(v, s.red[w]);
-    return v;
-}
+// The teacher's entries of the row, by one warp: ids to tc, exp((a - max) / T)
+// to tp, its exponent to tl, and for the loss (`student`) what the student's
+// exponents are taken of at them to tx.
+struct DsTeacher {
+    float *tp, *tl, *tx;
+    int* tc;
+    float log_psum;
+    bool bad;
+};
 
 template <bool CAP>
-__device__ __forceinline__ void ds_load8(const DsArgs& a, uint4 v, float (&z)[8]) {
-    v.x ^= a.flip, v.y ^= a.flip, v.z ^= a.flip, v.w ^= a.flip;
-    widen8(v, z);
-    if (CAP) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = ds_t<true>(a, z[e]);
-    }
-}
-
-// One row a cluster.
-template <bool GRAD, bool CAP>
-__global__ void __launch_bounds__(kDsMaxThreads) distill_kernel(const DsArgs a) {
-    extern __shared__ __align__(16) unsigned char raw[];
-    __shared__ DsShared sh;
-    let_next();
-    const int T = blockDim.x, tid = threadIdx.x;
-    const uint32_t rank = ds_rank();
-    const long long row = blockIdx.x >> a.log_cluster;
-    const long long c0 = static_cast<long long>(rank) * a.slice;
-    const int n = static_cast<int>(max(0LL, min(static_cast<long long>(a.slice), a.V - c0)));  // this block's logits
-    const int nvec = (n + 7) >> 3, nfull = n >> 3;
-    uint4* slice = reinterpret_cast<uint4*>(raw);
-    float* tp = reinterpret_cast<float*>(raw + static_cast<size_t>(a.slice) * 2);  // teacher's p
-    float* tx = tp + a.K;                                                         // rank 0: log q + its constant
-    int* tc = reinterpret_cast<int*>(tx + a.K);                                   // teacher's ids
-    const __nv_bfloat16* z = a.z + row * a.ld + c0;
-    const bool ignored = a.labels != nullptr && a.labels[row] == a.ignore;
-    if (ignored) {  // the same for the whole cluster
-        wait_prior();
-        if (GRAD) {
-            __nv_bfloat16* dz = a.dz + row * a.ld + c0;
-            for (int j = tid; j < nfull; j += T) reinterpret_cast<uint4*>(dz)[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (tid < n - 8 * nfull) dz[8 * nfull + tid] = __float2bfloat16(0.0f);
-        }
-        if (a.loss != nullptr && rank == 0 && tid == 0) a.loss[row] = 0.0f;
-        return;
-    }
-    ds_cluster_arrive();
-    const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(slice));
-    for (int j = tid; j < nfull; j += T)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sbase + 16u * j), "l"(z + 8 * j) : "memory");
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (nfull < nvec && tid == nfull % T) {  // the thread that reads the last, partial vector: V need not be a
-        uint16_t* last = reinterpret_cast<uint16_t*>(slice + nfull);  // multiple of 8, nor the row padded
-        for (int e = 0; e < 8; ++e)
-            last[e] = e < n - 8 * nfull ? __bfloat16_as_ushort(z[8 * nfull + e]) : static_cast<uint16_t>(0);
-    }
-
-    // The teacher's softmax over its entries, by every block for itself; block
-    // 0 also fetches the student's logits at them for the loss.
-    if (tid == 0) sh.bad = 0;
-    __syncthreads();
+__device__ __forceinline__ void ds_teacher(const DsArgs& a, DsShared& sh, DsTeacher& t, long long row, bool student) {
+    const int lane = threadIdx.x & 31;
     float amax = -3.4028234663852886e38f;  // fp32's lowest, which a teacher's mask may hold
-    bool any = false;
-    for (int i = tid; i < a.K; i += T) {
+    bool any = false, bad = false;
+#pragma unroll 4
+    for (int i = lane; i < a.K; i += 32) {
         const long long at = row * a.K + i;
         const long long id = a.ids_i64 ? static_cast<const long long*>(a.ids)[at] : static_cast<const int*>(a.ids)[at];
         const float v = a.values_f32 ? static_cast<const float*>(a.values)[at]
                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.values)[at]);
         const bool in = id >= 0 && id < a.V;
-        if (id < -1 || id >= a.V) sh.bad = 1;
-        tc[i] = in ? static_cast<int>(id) : -1;
-        tp[i] = v;
+        bad = bad || id < -1 || id >= a.V;
+        t.tc[i] = in ? static_cast<int>(id) : -1;
+        t.tl[i] = v;
         if (in) {
             amax = fmaxf(amax, v);
             any = any || !(v == -INFINITY);
-        }
-        if (rank == 0 && in) {
-            float zc = __bfloat162float(a.z[row * a.ld + id]);
-            if (a.flip) zc = -zc;
-            tx[i] = CAP ? a.cap * tanhf(a.scale / a.cap * zc) : zc;
+            if (student) {
+                float z = __bfloat162float(a.z[row * a.ld + id]);
+                if (a.flip) z = -z;
+                t.tx[i] = CAP ? -1.0f / (1.0f + expf(2.0f * (a.scale / a.cap * z))) : z;
+            }
         }
     }
-    const float A = ds_block_max(sh, amax);
-    const bool live = __syncthreads_or(any);
+    amax = ds_warp_max(amax);
     float psum = 0.0f;
-    for (int i = tid; i < a.K; i += T)
-        if (tc[i] >= 0) psum += expf((tp[i] - A) * a.inv_T);
-    psum = ds_block_sum(sh, psum);
-    const float logp0 = logf(psum), inv_psum = 1.0f / psum;
-
-    // The slice's maximum and sum.
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    float m = kDsLowest, s = 0.0f;
-    {
-        uint32_t m2 = 0xFF7FFF7Fu;  // two of bf16's lowest
-        for (int j = tid; j < nvec; j += T) {
-            const uint4 v = slice[j];
-            const uint32_t w[4] = {v.x ^ a.flip, v.y ^ a.flip, v.z ^ a.flip, v.w ^ a.flip};
-            if (j < nfull) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w[i]));
-            } else {
-                for (int e = 0; e < n - 8 * nfull; ++e)
-                    m = fmaxf(m, __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16));
-            }
-        }
-        m = fmaxf(m, fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xFFFF0000u)));
-        if (CAP) m = ds_t<true>(a, m);
+    for (int i = lane; i < a.K; i += 32) {
+        const float l = (t.tl[i] - amax) * a.inv_T, e = t.tc[i] >= 0 ? expf(l) : 0.0f;
+        t.tl[i] = l;
+        t.tp[i] = e;
+        psum += e;
     }
-    for (int j = tid; j < nvec; j += T) {
-        float x[8];
-        ds_load8<CAP>(a, slice[j], x);
-        if (j >= nfull)
-            for (int e = 0; e < 8; ++e)
-                if (e >= n - 8 * nfull) x[e] = -INFINITY;
-        const uint64_t mm = f2_packf(m, m), kk = f2_packf(a.k, a.k);
-        float part[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float lo, hi;
-            f2_unpack(f2_mul(f2_sub(f2_packf(x[2 * i], x[2 * i + 1]), mm), kk), lo, hi);
-            part[i] = ds_ex2(lo) + ds_ex2(hi);
-        }
-        s += (part[0] + part[1]) + (part[2] + part[3]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        ds_merge(m, s, m2, s2, a.k);
-    }
-    if ((tid & 31) == 0) sh.warp[tid >> 5] = make_float2(m, s);
-    __syncthreads();
-    ds_cluster_wait();  // every block of the cluster runs: its shared memory may be written
-    const uint32_t cluster = 1u << a.log_cluster;
-    if (tid < static_cast<int>(cluster)) {
-        m = sh.warp[0].x, s = sh.warp[0].y;
-        for (int w = 1; w < T / 32; ++w) ds_merge(m, s, sh.warp[w].x, sh.warp[w].y, a.k);
-        uint32_t to;
-        const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(&sh.all[rank]));
-        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(tid));
-        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(m), "f"(s) : "memory");
-    }
-    ds_cluster_arrive();
-    ds_cluster_wait();
-    m = sh.all[0].x, s = sh.all[0].y;
-    for (uint32_t r = 1; r < cluster; ++r) ds_merge(m, s, sh.all[r].x, sh.all[r].y, a.k);
-
-    wait_prior();  // the factor may come from the kernel before
-    if (rank == 0 && a.loss != nullptr) {
-        const float logq0 = logf(s);
-        float part = 0.0f;
-        for (int i = tid; i < a.K; i += T) {
-            if (tc[i] < 0) continue;
-            const float la = (tp[i] - A) * a.inv_T - logp0, p = expf((tp[i] - A) * a.inv_T) * inv_psum;
-            if (p != 0.0f) part += p * (la - ((tx[i] - m) * a.kn - logq0));
-        }
-        part = ds_block_sum(sh, part);
-        if (tid == 0) {
-            const bool bad = sh.bad != 0;
-            if (bad) atomicExch(a.status, -1);
-            a.loss[row] = bad ? __int_as_float(0x7fc00000) : (live ? a.T * a.T * part : 0.0f);
-        }
-    } else if (rank == 0 && tid == 0 && sh.bad) {
-        atomicExch(a.status, -1);
-    }
-    if (!GRAD) return;
-
-    float g = a.T * a.scale;
-    if (a.flip) g = -g;
-    if (a.dloss != nullptr) g *= a.dloss[row * a.dloss_stride];
-    if (a.factor != nullptr) g *= a.factor[1];
-    if (!live) g = 0.0f;
-    const float gs = live ? g / s : 0.0f;
-    const float inv_cap = CAP ? 1.0f / a.cap : 0.0f;
-    __nv_bfloat16* dz = a.dz + row * a.ld + c0;
-    for (int j = tid; j < nvec; j += T) {
-        float x[8], d[8];
-        ds_load8<CAP>(a, slice[j], x);
-        const uint64_t mm = f2_packf(m, m), kk = f2_packf(a.k, a.k), gg = f2_packf(gs, gs);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint64_t x2 = f2_packf(x[2 * i], x[2 * i + 1]);
-            float lo, hi;
-            f2_unpack(f2_mul(f2_sub(x2, mm), kk), lo, hi);
-            uint64_t d2 = f2_mul(f2_packf(ds_ex2(lo), ds_ex2(hi)), gg);
-            if (CAP) {  // times 1 - (t / cap)^2
-                const uint64_t th = f2_mul(x2, f2_packf(inv_cap, inv_cap));
-                const uint64_t nth = f2_mul(x2, f2_packf(-inv_cap, -inv_cap));
-                d2 = f2_mul(d2, f2_fma(th, nth, f2_packf(1.0f, 1.0f)));
-            }
-            f2_unpack(d2, d[2 * i], d[2 * i + 1]);
-        }
-        if (!live)
-            for (int e = 0; e < 8; ++e) d[e] = 0.0f;
-        const uint4 o = round8(d);
-        if (j < nfull) {
-            __stcs(reinterpret_cast<uint4*>(dz) + j, o);
-        } else {
-            const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-            for (int e = 0; e < n - 8 * nfull; ++e)
-                dz[8 * j + e] = __ushort_as_bfloat16(static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1]));
-        }
-    }
-    if (!live) return;
-    __syncthreads();  // the elements below are written a second time
-    for (int i = tid; i < a.K; i += T) {
-        const int c = tc[i];
-        const long long at = c - c0;
-        if (c < 0 || at < 0 || at >= n) continue;
-        bool first = true;
-        float p = 0.0f;
-        for (int o = 0; o < a.K; ++o) {
-            if (tc[o] != c) continue;
-            if (o < i) first = false;
-            p += expf((tp[o] - A) * a.inv_T) * inv_psum;
-        }
-        if (!first) continue;  // the first entry of an id writes for all of them
-        float x = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(slice)[at]);
-        if (a.flip) x = -x;
-        x = ds_t<CAP>(a, x);
-        float d = (ds_ex2((x - m) * a.k) / s - p) * g;
-        if (CAP) d *= 1.0f - (x * inv_cap) * (x * inv_cap);
-        dz[at] = __float2bfloat16(d);
+    psum = ds_warp_sum(psum);
+    t.log_psum = logf(psum);
+    t.bad = __any_sync(0xffffffffu, bad);
+    any = __any_sync(0xffffffffu, any);
+    if (lane == 0) {
+        sh.inv_psum = 1.0f / psum;
+        sh.live = any;
     }
 }
 
-// factor[1] = 1 / (rows whose label is not ignore_index) for the mean, else 1.
-constexpr int kDsReduceThreads = 1024;
-__global__ void __launch_bounds__(kDsReduceThreads) distill_count_kernel(const long long* labels, long long N,
-                                                                         long long ignore, bool mean, float* out) {
+// The rows' losses reduced by one block, in fp64 and a fixed order.
+__device__ __forceinline__ void ds_reduce(const DsArgs& a, double* sum) {
+    const int T = blockDim.x, tid = threadIdx.x;
+    int* cnt = reinterpret_cast<int*>(sum + T);
+    __threadfence();
+    double v = 0.0;
+    int c = 0;
+#pragma unroll 4
+    for (long long r = tid; r < a.N; r += T) {
+        v += static_cast<double>(__ldcg(a.loss + r));
+        if (a.mean) c += a.labels == nullptr || a.labels[r] != a.ignore;
+    }
+    sum[tid] = v;
+    cnt[tid] = c;
+    __syncthreads();
+    if (tid < 32) {
+        for (int i = tid + 32; i < T; i += 32) v += sum[i], c += cnt[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            v += __shfl_xor_sync(0xffffffffu, v, o);
+            c += __shfl_xor_sync(0xffffffffu, c, o);
+        }
+        if (tid == 0) a.out[0] = static_cast<float>(a.mean ? v / static_cast<double>(c > 0 ? c : 1) : v);
+    }
+}
+
+// One row a cluster.
+template <bool GRAD, bool CAP>
+__global__ void __launch_bounds__(kDsMaxThreads, 3) distill_kernel(const DsArgs a) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    __shared__ DsShared sh;
     let_next();
-    __shared__ int cnt[kDsReduceThreads / 32];
+    const int T = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = ds_rank(), cluster = 1u << a.log_cluster;
+    const long long row = blockIdx.x >> a.log_cluster;
+    const long long c0 = static_cast<long long>(rank) * a.slice;
+    const int n = static_cast<int>(max(0LL, min(static_cast<long long>(a.slice), a.V - c0)));  // this block's logits
+    const int nvec = (n + 7) >> 3, nfull = n >> 3;
+    const int part = (nvec + T * kDsParts - 1) / (T * kDsParts);  // a thread's vectors of a part
+    uint4* slice = reinterpret_cast<uint4*>(raw);
+    const __nv_bfloat16* z = a.z + row * a.ld + c0;
+    const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(slice));
+#pragma unroll
+    for (int g = 0; g < kDsParts; ++g) {
+        for (int i = 0; i < part; ++i) {
+            const int j = tid + (g * part + i) * T;
+            if (j < nfull)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sbase + 16u * j), "l"(z + 8 * j) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    ds_cluster_arrive();
+    const bool ignored = a.labels != nullptr && a.labels[row] == a.ignore;  // the same for the whole cluster
+    DsTeacher t{};
+    t.tp = reinterpret_cast<float*>(raw + static_cast<size_t>(a.slice) * 2);
+    t.tl = t.tp + a.K;
+    t.tx = t.tl + a.K;
+    t.tc = reinterpret_cast<int*>(t.tx + a.K);
+    const bool wants_loss = rank == 0 && a.loss != nullptr;
+    const int ntail = n - 8 * nfull;
+    __nv_bfloat16* dz = GRAD ? a.dz + row * a.ld + c0 : nullptr;
+    if (ignored) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        wait_prior();
+        if (GRAD) {
+            for (int j = tid; j < nfull; j += T) reinterpret_cast<uint4*>(dz)[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (tid < ntail) dz[8 * nfull + tid] = __float2bfloat16(0.0f);
+        }
+        ds_cluster_wait();
+        if (wants_loss && tid == 0) a.loss[row] = 0.0f;
+    } else {
+        // V need not be a multiple of 8, nor the row padded: the logits behind
+        // the last whole vector go to one thread each
+        float xt = 0.0f;
+        if (tid < ntail) {
+            const __nv_bfloat16 zt = z[8 * nfull + tid];
+            reinterpret_cast<__nv_bfloat16*>(slice)[8 * nfull + tid] = zt;
+            xt = ds_arg<CAP>(a, a.flip ? -__bfloat162float(zt) : __bfloat162float(zt));
+        }
+        if (warp == 0) ds_teacher<CAP>(a, sh, t, row, wants_loss);
+
+        // The slice's maximum and sum.  A batch's maximum comes first, so that
+        // the running sum is rescaled at most once a batch.
+        float m = CAP ? -1.0f : kDsLowest, s = 0.0f;
+        const uint64_t kk = f2_packf(a.k, a.k);
+#pragma unroll
+        for (int g = 0; g < kDsParts; ++g) {
+            if (g == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
+            if (g == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
+            if (g == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            if (g == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
+            for (int i = 0; i < part; i += kDsBatch) {
+                const int j0 = tid + (g * part + i) * T;
+                const int stop = min(nfull, tid + (g + 1) * part * T);  // of this part
+                uint4 v[kDsBatch];
+                uint32_t m2 = 0xFF7FFF7Fu;  // two of bf16's lowest
+#pragma unroll
+                for (int b = 0; b < kDsBatch; ++b) {
+                    if (j0 + b * T >= stop) break;
+                    v[b] = ds_signed(a, slice[j0 + b * T]);
+                    ds_max(m2, v[b]);
+                }
+                if (j0 >= stop) break;
+                const float mb = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xFFFF0000u));
+                const float xb = ds_arg<CAP>(a, mb);
+                if (xb > m) {
+                    s *= ds_ex2((m - xb) * a.k);
+                    m = xb;
+                }
+                const uint64_t mm = f2_packf(m, m);
+#pragma unroll
+                for (int b = 0; b < kDsBatch; ++b) {
+                    if (j0 + b * T >= stop) break;
+                    float x[8];
+                    ds_args8<CAP>(a, v[b], x);
+                    uint64_t e[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float lo, hi;
+                        f2_unpack(f2_mul(f2_sub(f2_packf(x[2 * q], x[2 * q + 1]), mm), kk), lo, hi);
+                        e[q] = f2_packf(ds_ex2(lo), ds_ex2(hi));
+                    }
+                    float lo, hi;
+                    f2_unpack(f2_add(f2_add(e[0], e[1]), f2_add(e[2], e[3])), lo, hi);
+                    s += lo + hi;
+                }
+            }
+        }
+        if (tid < ntail) {
+            const float M = fmaxf(m, xt);
+            s = s * ds_ex2((m - M) * a.k) + ds_ex2((xt - M) * a.k);
+            m = M;
+        }
+        float M = ds_warp_max(m);
+        s = ds_warp_sum(s * ds_ex2((m - M) * a.k));
+        if (lane == 0) sh.warp[warp] = make_float2(M, s);
+        __syncthreads();
+        ds_cluster_wait();  // every block of the cluster runs: its shared memory may be written
+        if (warp == 0) {
+            const float2 w = lane < T / 32 ? sh.warp[lane] : make_float2(CAP ? -1.0f : kDsLowest, 0.0f);
+            M = ds_warp_max(w.x);
+            s = ds_warp_sum(w.y * ds_ex2((w.x - M) * a.k));
+            if (lane < static_cast<int>(cluster)) {
+                uint32_t to;
+                const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(&sh.all[rank]));
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(lane));
+                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(M), "f"(s) : "memory");
+            }
+            __syncwarp();
+        }
+        ds_cluster_arrive();
+        ds_cluster_wait();
+        m = sh.all[0].x;
+        for (uint32_t r = 1; r < cluster; ++r) m = fmaxf(m, sh.all[r].x);
+        s = 0.0f;
+        for (uint32_t r = 0; r < cluster; ++r) s += sh.all[r].y * ds_ex2((sh.all[r].x - m) * a.k);
+
+        wait_prior();  // the factor may come from the kernel before
+        const bool live = sh.live != 0;
+        if (warp == 0) {
+            if (wants_loss) {
+                const float log_s = logf(s), inv_psum = sh.inv_psum;
+                float sum = 0.0f;
+                for (int i = lane; i < a.K; i += 32) {
+                    const float p = t.tp[i] * inv_psum;
+                    if (p != 0.0f) sum += p * ((t.tl[i] - t.log_psum) - ((t.tx[i] - m) * a.kn - log_s));
+                }
+                sum = ds_warp_sum(sum);
+                if (lane == 0)
+                    a.loss[row] = t.bad ? __int_as_float(0x7fc00000) : (live ? a.T * a.T * sum : 0.0f);
+            }
+            if (t.bad && rank == 0 && lane == 0) atomicExch(a.status, -1);
+        }
+        if (GRAD && !live) {
+            for (int j = tid; j < nfull; j += T) reinterpret_cast<uint4*>(dz)[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (tid < ntail) dz[8 * nfull + tid] = __float2bfloat16(0.0f);
+        }
+        if (GRAD && live) {
+            float g = a.T * (a.flip ? -a.scale : a.scale);
+            if (a.dloss != nullptr) g *= a.dloss[row * a.dloss_stride];
+            if (a.factor != nullptr) g *= a.factor[1];
+            const float gs = g / s;
+            const uint64_t mm = f2_packf(m, m), gg = f2_packf(CAP ? -4.0f * gs : gs, CAP ? -4.0f * gs : gs);
+#pragma unroll 2
+            for (int j = tid; j < nfull; j += T) {
+                float x[8], d[8];
+                ds_args8<CAP>(a, ds_signed(a, slice[j]), x);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint64_t x2 = f2_packf(x[2 * q], x[2 * q + 1]);
+                    float lo, hi;
+                    f2_unpack(f2_mul(f2_sub(x2, mm), kk), lo, hi);
+                    uint64_t d2 = f2_mul(f2_packf(ds_ex2(lo), ds_ex2(hi)), gg);
+                    if (CAP) d2 = f2_mul(d2, f2_fma(x2, x2, x2));  // 4 r (1 - r) = -4 (x^2 + x)
+                    f2_unpack(d2, d[2 * q], d[2 * q + 1]);
+                }
+                __stcs(reinterpret_cast<uint4*>(dz) + j, round8(d));
+            }
+            const auto one = [&](float x, float p) {
+                const float d = (ds_ex2((x - m) * a.k) / s - p) * g;
+                return __float2bfloat16(CAP ? -4.0f * d * fmaf(x, x, x) : d);
+            };
+            if (tid < ntail) dz[8 * nfull + tid] = one(xt, 0.0f);
+            __syncthreads();  // the teacher's elements are written a second time
+            const float inv_psum = sh.inv_psum;
+            for (int i = tid; i < a.K; i += T) {
+                const int c = t.tc[i];
+                const long long at = c - c0;
+                if (c < 0 || at < 0 || at >= n) continue;
+                bool first = true;  // the first entry of an id writes for all of them
+                float p = 0.0f;
+                for (int o = 0; o < a.K; ++o) {
+                    if (t.tc[o] != c) continue;
+                    first = first && o >= i;
+                    p += t.tp[o] * inv_psum;
+                }
+                if (!first) continue;
+                const float zc = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(slice)[at]);
+                dz[at] = one(ds_arg<CAP>(a, a.flip ? -zc : zc), p);
+            }
+        }
+    }
+    if (a.out == nullptr || rank != 0) return;
+    if (tid == 0) {
+        __threadfence();
+        sh.last = atomicAdd(a.counter, 1u) == static_cast<uint32_t>(a.N - 1);
+    }
+    __syncthreads();
+    if (sh.last) ds_reduce(a, reinterpret_cast<double*>(raw));
+}
+
+// out[1] = d out[0] / d loss of a row that takes part: 1 / (rows whose label
+// is not ignore_index) for the mean, else 1; and the counter of rows done.
+constexpr int kDsCountThreads = 1024;
+__global__ void __launch_bounds__(kDsCountThreads) distill_count_kernel(const long long* labels, long long N,
+                                                                        long long ignore, int mean, float* out,
+                                                                        uint32_t* counter) {
+    let_next();
+    __shared__ int cnt[kDsCountThreads / 32];
     int c = 0;
     if (mean)
-        for (long long r = threadIdx.x; r < N; r += kDsReduceThreads) c += labels == nullptr || labels[r] != ignore;
+        for (long long r = threadIdx.x; r < N; r += kDsCountThreads) c += labels == nullptr || labels[r] != ignore;
     c = __reduce_add_sync(0xffffffffu, c);
     if ((threadIdx.x & 31) == 0) cnt[threadIdx.x >> 5] = c;
     __syncthreads();
     if (threadIdx.x == 0) {
         long long all = 0;
-        for (int w = 0; w < kDsReduceThreads / 32; ++w) all += cnt[w];
+        for (int w = 0; w < kDsCountThreads / 32; ++w) all += cnt[w];
         out[1] = mean ? static_cast<float>(1.0 / static_cast<double>(all > 0 ? all : 1)) : 1.0f;
+        *counter = 0u;
     }
-}
-
-// out[0] = factor * sum of the rows' losses, in fp64: each thread adds every
-// 1024th row, then a fixed tree adds the threads.
-__global__ void __launch_bounds__(kDsReduceThreads) distill_reduce_kernel(const float* loss, long long N,
-                                                                          const long long* labels, long long ignore,
-                                                                          bool mean, float* out) {
-    __shared__ double sum[kDsReduceThreads];
-    __shared__ int cnt[kDsReduceThreads];
-    wait_prior();
-    double v = 0.0;
-    int c = 0;
-    for (long long r = threadIdx.x; r < N; r += kDsReduceThreads) {
-        v += static_cast<double>(loss[r]);
-        c += labels == nullptr || labels[r] != ignore;
-    }
-    sum[threadIdx.x] = v;
-    cnt[threadIdx.x] = c;
-    __syncthreads();
-    for (int h = kDsReduceThreads / 2; h > 0; h >>= 1) {
-        if (static_cast<int>(threadIdx.x) < h) {
-            sum[threadIdx.x] += sum[threadIdx.x + h];
-            cnt[threadIdx.x] += cnt[threadIdx.x + h];
-        }
-        __syncthreads();
-    }
-    if (threadIdx.x == 0)
-        out[0] = static_cast<float>(mean ? sum[0] / static_cast<double>(cnt[0] > 0 ? cnt[0] : 1) : sum[0]);
 }
 
 }  // namespace step

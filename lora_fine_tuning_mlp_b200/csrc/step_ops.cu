@@ -576,7 +576,8 @@ DsArgs ds_args(const lora_distill_shape* sh, const void* logits, const void* val
     a.flip = sh->logit_scale < 0.0f ? 0x80008000u : 0u;
     a.cap = sh->softcap;
     constexpr double kLog2e = 1.4426950408889634;
-    const double kn = (sh->softcap > 0.0f ? 1.0 : std::fabs(static_cast<double>(sh->logit_scale))) / sh->temperature;
+    const double kn = (sh->softcap > 0.0f ? 2.0 * sh->softcap : std::fabs(static_cast<double>(sh->logit_scale))) /
+                      sh->temperature;
     a.kn = static_cast<float>(kn);
     a.k = static_cast<float>(kn * kLog2e);
     if (sh->softcap > 0.0f) a.cap2 = static_cast<float>(2.0 * a.scale / sh->softcap * kLog2e);
@@ -596,11 +597,12 @@ int launch_distill(const char* name, DsArgs a, int sms, cudaStream_t st, bool af
         ++a.log_cluster;
     a.slice = static_cast<int>(slice(a.log_cluster));
     const int threads = std::min(kDsMaxThreads, std::max(64, a.slice / 8 / 4 / 32 * 32));
-    const size_t smem = static_cast<size_t>(a.slice) * 2 + static_cast<size_t>(a.K) * 12;
+    const size_t smem = std::max(static_cast<size_t>(a.slice) * 2 + static_cast<size_t>(a.K) * kDsEntryBytes,
+                                 static_cast<size_t>(threads) * 12);  // 12: the reduction's sums and counts
     const bool grad = a.dz != nullptr, cap = a.cap > 0.0f;
     auto kernel = grad ? (cap ? distill_kernel<true, true> : distill_kernel<true, false>)
                        : (cap ? distill_kernel<false, true> : distill_kernel<false, false>);
-    STEP_TRY(allow_smem(kernel, kDsMaxV / kDsMaxCluster * 2 + kDsMaxK * 12));
+    STEP_TRY(allow_smem(kernel, kDsMaxV / kDsMaxCluster * 2 + kDsMaxK * kDsEntryBytes));
     return launch(name, kernel, dim3(static_cast<unsigned>(a.N << a.log_cluster)), threads, smem, st, after_own,
                   1 << a.log_cluster, a);
 }
@@ -663,9 +665,7 @@ int lora_distill_backward_reduced(const lora_distill_shape* shape, const void* l
 
 int lora_distill_sizes(const lora_distill_shape* shape, size_t* workspace_bytes) {
     STEP_TRY(validate_distill(shape));
-    Carver c;
-    c.take(static_cast<size_t>(shape->N) * 4);
-    if (workspace_bytes) *workspace_bytes = c.off;
+    if (workspace_bytes) *workspace_bytes = kAlign + static_cast<size_t>(shape->N) * 4;
     return LORA_MLP_OK;
 }
 
@@ -687,14 +687,15 @@ int lora_distill_loss(const lora_distill_shape* shape, const void* logits, const
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool mean = reduction == LORA_DISTILL_REDUCTION_MEAN;
     DsArgs a = ds_args(shape, logits, values, ids, labels, di.status);
-    STEP_TRY(launch("DISTILL_count", distill_count_kernel, dim3(1), kDsReduceThreads, 0, st, false, 1, a.labels, a.N,
-                    a.ignore, mean, out));
-    a.loss = static_cast<float*>(workspace);
+    a.counter = static_cast<uint32_t*>(workspace);
+    a.loss = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAlign);
     a.dz = static_cast<__nv_bfloat16*>(dlogits);
+    a.out = out;
     a.factor = out;
-    STEP_TRY(launch_distill(dlogits != nullptr ? "DISTILL_loss_grad" : "DISTILL_fwd", a, di.sms, st, true));
-    return launch("DISTILL_reduce", distill_reduce_kernel, dim3(1), kDsReduceThreads, 0, st, true, 1,
-                  static_cast<const float*>(a.loss), a.N, a.labels, a.ignore, mean, out);
+    a.mean = mean;
+    STEP_TRY(launch("DISTILL_count", distill_count_kernel, dim3(1), kDsCountThreads, 0, st, false, 1, a.labels, a.N,
+                    a.ignore, a.mean, out, a.counter));
+    return launch_distill(dlogits != nullptr ? "DISTILL_loss_grad" : "DISTILL_fwd", a, di.sms, st, true);
 }
 
 }  // extern "C"
