@@ -13,13 +13,15 @@
 // a multiprocessor overlap one's loads with another's arithmetic.
 //
 // Every thread copies the 16-byte vectors that it later reads (cp.async), so
-// the loads need no barrier, and takes them up in four parts as they arrive.
-// Sums are taken of 2^((z - m) k) with the difference formed first: exact next
-// to the maximum, and rows filled with bf16's lowest value or with large
-// logits neither overflow nor vanish.  With softcapping, t = cap tanh(s z /
-// cap) = cap - 2 cap r with r = 1 / (1 + 2^(cap2 z)): exponents are taken of
-// -r, dt/dz = 4 s r (1 - r) has no cancellation where tanh saturates, and four
-// logits share one reciprocal.
+// the loads need no barrier, and takes them up in four parts as they arrive;
+// one warp beside them takes the teacher's softmax.  Exponents are in base 2
+// and relative to fl(m k) for the maximum m: fma(z, k, -fl(m k)) rounds once,
+// and sums relative to that very number are exact in it.  Where m k is out of
+// fma's range (rows filled with bf16's lowest value, say) the difference z - m
+// is formed first.  With softcapping, t = cap tanh(s z / cap) = cap - 2 cap r
+// with r = 1 / (1 + 2^(cap2 z)): exponents are taken of -r, dt/dz = 4 s r (1 -
+// r) has no cancellation where tanh saturates, and four logits share one
+// reciprocal.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -30,7 +32,7 @@
 namespace lmlp {
 namespace step {
 
-constexpr int kDsMaxThreads = 256;
+constexpr int kDsMaxThreads = 256;  // that work on the slice; a warp for the teacher comes on top
 constexpr int kDsMaxCluster = 8;
 constexpr int kDsMaxK = 1024;
 constexpr int kDsParts = 4;   // of a thread's vectors, waited for one after the other
@@ -53,12 +55,13 @@ struct DsArgs {
     float scale, cap;     // s with its sign taken off (see flip), cap or 0
     uint32_t flip;        // 0x80008000 where s is negative: z and dz change sign
     float k;              // base-2 exponent of a unit of z: s log2(e) / T; of a unit of -r: 2 cap log2(e) / T
-    float kn;             // the natural exponent of the same
     float cap2;           // 2 s / cap * log2(e)
     float* loss;          // may be null
     float* out;           // the reduced loss, or null
     uint32_t* counter;    // rows done, zero before the launch (with out)
     int mean;
+    int threads;          // that work on the slice
+    int Kp;               // K rounded up to 4
     const float* dloss;   // [N], stride 0 or 1 (null: 1)
     long long dloss_stride;
     const float* factor;  // factor[1] multiplies it (null: 1)
@@ -135,6 +138,23 @@ __device__ __forceinline__ void ds_max(uint32_t& m2, const uint4& v) {
     asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v.w));
 }
 
+// Whether m k is out of the range in which z k - fl(m k) is formed by one fma.
+template <bool CAP>
+__device__ __forceinline__ bool ds_far(float m, float k) {
+    return !CAP && !(fabsf(m * k) < 1.0e30f);
+}
+// A term of a sum that is relative to m.
+template <bool CAP>
+__device__ __forceinline__ float ds_rel(float x, float m, float k) {
+    return ds_far<CAP>(m, k) ? ds_ex2((x - m) * k) : ds_ex2(fmaf(x, k, -__fmul_rn(m, k)));
+}
+// What turns a sum relative to m into one relative to M >= m: 2^(fl(m k) -
+// fl(M k)), both products rounded (1 where m = M).
+template <bool CAP>
+__device__ __forceinline__ float ds_shift(float m, float M, float k) {
+    return ds_far<CAP>(M, k) ? ds_ex2((m - M) * k) : ds_ex2(__fmul_rn(m, k) - __fmul_rn(M, k));
+}
+
 struct DsShared {
     float2 warp[32];            // (max, sum) of each warp
     float2 all[kDsMaxCluster];  // ... of each block of the cluster, written by all of them
@@ -159,12 +179,12 @@ __device__ __forceinline__ void ds_teacher(const DsArgs& a, DsShared& sh, DsTeac
     float amax = -3.4028234663852886e38f;  // fp32's lowest, which a teacher's mask may hold
     bool any = false, bad = false;
 #pragma unroll 4
-    for (int i = lane; i < a.K; i += 32) {
-        const long long at = row * a.K + i;
+    for (int i = lane; i < a.Kp; i += 32) {
+        const long long at = row * a.K + min(i, a.K - 1);
         const long long id = a.ids_i64 ? static_cast<const long long*>(a.ids)[at] : static_cast<const int*>(a.ids)[at];
         const float v = a.values_f32 ? static_cast<const float*>(a.values)[at]
                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.values)[at]);
-        const bool in = id >= 0 && id < a.V;
+        const bool in = i < a.K && id >= 0 && id < a.V;
         bad = bad || id < -1 || id >= a.V;
         t.tc[i] = in ? static_cast<int>(id) : -1;
         t.tl[i] = v;
@@ -180,7 +200,7 @@ __device__ __forceinline__ void ds_teacher(const DsArgs& a, DsShared& sh, DsTeac
     }
     amax = ds_warp_max(amax);
     float psum = 0.0f;
-    for (int i = lane; i < a.K; i += 32) {
+    for (int i = lane; i < a.Kp; i += 32) {
         const float l = (t.tl[i] - amax) * a.inv_T, e = t.tc[i] >= 0 ? expf(l) : 0.0f;
         t.tl[i] = l;
         t.tp[i] = e;
@@ -193,6 +213,50 @@ __device__ __forceinline__ void ds_teacher(const DsArgs& a, DsShared& sh, DsTeac
     if (lane == 0) {
         sh.inv_psum = 1.0f / psum;
         sh.live = any;
+    }
+}
+
+// A batch's exponentials added up: sum of 2^(x k - m k) over the vectors j0, j0
+// + T, ... below `stop`.
+template <bool CAP, bool FAR>
+__device__ __forceinline__ float ds_batch_sum(const DsArgs& a, const uint4 (&v)[kDsBatch], int j0, int stop, float m) {
+    const float c = FAR ? m : -__fmul_rn(m, a.k);
+    float s = 0.0f;
+#pragma unroll
+    for (int b = 0; b < kDsBatch; ++b) {
+        if (j0 + b * a.threads >= stop) break;
+        float x[8];
+        ds_args8<CAP>(a, v[b], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = ds_ex2(FAR ? (x[e] - c) * a.k : fmaf(x[e], a.k, c));
+        s += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    }
+    return s;
+}
+
+// The gradient of the whole vectors, the teacher's part left out: gs 2^(x k -
+// m k) dt/dz.  The factor gs goes into the exponent (its sign apart): it is
+// off by 2^-24 of that exponent, far below the rounding to bf16.
+template <bool CAP, bool FAR>
+__device__ __forceinline__ void ds_grad(const DsArgs& a, const uint4* slice, uint4* dz, int nfull, float m, float gs) {
+    const float c = FAR ? m : log2f(fabsf(CAP ? 4.0f * gs : gs)) - __fmul_rn(m, a.k);
+    const uint32_t sign = !FAR && ((gs < 0.0f) != CAP) ? 0x80008000u : 0u;  // x^2 + x below is negative
+#pragma unroll 2
+    for (int j = threadIdx.x; j < nfull; j += a.threads) {
+        float x[8];
+        ds_args8<CAP>(a, ds_signed(a, slice[j]), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (FAR) {
+                x[e] = ds_ex2((x[e] - c) * a.k) * gs;
+            } else {
+                const float y = ds_ex2(fmaf(x[e], a.k, c));
+                x[e] = CAP ? y * fmaf(x[e], x[e], x[e]) : y;  // r (1 - r) = -(x^2 + x)
+            }
+        }
+        uint4 o = round8(x);
+        if (sign) o = make_uint4(o.x ^ sign, o.y ^ sign, o.z ^ sign, o.w ^ sign);
+        __stcs(dz + j, o);
     }
 }
 
@@ -224,120 +288,99 @@ __device__ __forceinline__ void ds_reduce(const DsArgs& a, double* sum) {
 
 // One row a cluster.
 template <bool GRAD, bool CAP>
-__global__ void __launch_bounds__(kDsMaxThreads, 3) distill_kernel(const DsArgs a) {
+__global__ void __launch_bounds__(kDsMaxThreads + 32, 3) distill_kernel(const DsArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ DsShared sh;
     let_next();
-    const int T = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int T = a.threads, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool teaches = tid >= T;  // the last warp
     const uint32_t rank = ds_rank(), cluster = 1u << a.log_cluster;
     const long long row = blockIdx.x >> a.log_cluster;
     const long long c0 = static_cast<long long>(rank) * a.slice;
     const int n = static_cast<int>(max(0LL, min(static_cast<long long>(a.slice), a.V - c0)));  // this block's logits
-    const int nvec = (n + 7) >> 3, nfull = n >> 3;
-    const int part = (nvec + T * kDsParts - 1) / (T * kDsParts);  // a thread's vectors of a part
+    const int nfull = n >> 3, ntail = n & 7;
+    const int part = (nfull + T * kDsParts - 1) / (T * kDsParts);  // a thread's vectors of a part
     uint4* slice = reinterpret_cast<uint4*>(raw);
     const __nv_bfloat16* z = a.z + row * a.ld + c0;
-    const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(slice));
+    if (!teaches) {
+        const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(slice));
 #pragma unroll
-    for (int g = 0; g < kDsParts; ++g) {
-        for (int i = 0; i < part; ++i) {
-            const int j = tid + (g * part + i) * T;
-            if (j < nfull)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sbase + 16u * j), "l"(z + 8 * j) : "memory");
+        for (int g = 0; g < kDsParts; ++g) {
+            for (int i = 0; i < part; ++i) {
+                const int j = tid + (g * part + i) * T;
+                if (j < nfull)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sbase + 16u * j), "l"(z + 8 * j)
+                                 : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
     }
     ds_cluster_arrive();
     const bool ignored = a.labels != nullptr && a.labels[row] == a.ignore;  // the same for the whole cluster
-    DsTeacher t{};
-    t.tp = reinterpret_cast<float*>(raw + static_cast<size_t>(a.slice) * 2);
-    t.tl = t.tp + a.K;
-    t.tx = t.tl + a.K;
-    t.tc = reinterpret_cast<int*>(t.tx + a.K);
     const bool wants_loss = rank == 0 && a.loss != nullptr;
-    const int ntail = n - 8 * nfull;
     __nv_bfloat16* dz = GRAD ? a.dz + row * a.ld + c0 : nullptr;
+    bool zeros = ignored;
     if (ignored) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         wait_prior();
-        if (GRAD) {
-            for (int j = tid; j < nfull; j += T) reinterpret_cast<uint4*>(dz)[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (tid < ntail) dz[8 * nfull + tid] = __float2bfloat16(0.0f);
-        }
         ds_cluster_wait();
         if (wants_loss && tid == 0) a.loss[row] = 0.0f;
     } else {
-        // V need not be a multiple of 8, nor the row padded: the logits behind
-        // the last whole vector go to one thread each
-        float xt = 0.0f;
-        if (tid < ntail) {
-            const __nv_bfloat16 zt = z[8 * nfull + tid];
-            reinterpret_cast<__nv_bfloat16*>(slice)[8 * nfull + tid] = zt;
-            xt = ds_arg<CAP>(a, a.flip ? -__bfloat162float(zt) : __bfloat162float(zt));
-        }
-        if (warp == 0) ds_teacher<CAP>(a, sh, t, row, wants_loss);
-
-        // The slice's maximum and sum.  A batch's maximum comes first, so that
-        // the running sum is rescaled at most once a batch.
-        float m = CAP ? -1.0f : kDsLowest, s = 0.0f;
-        const uint64_t kk = f2_packf(a.k, a.k);
+        DsTeacher t{};
+        t.tp = reinterpret_cast<float*>(raw + static_cast<size_t>(a.slice) * 2);
+        t.tl = t.tp + a.Kp;
+        t.tx = t.tl + a.Kp;
+        t.tc = reinterpret_cast<int*>(t.tx + a.Kp);
+        float m = CAP ? -1.0f : kDsLowest, s = 0.0f, xt = 0.0f;
+        if (teaches) {
+            ds_teacher<CAP>(a, sh, t, row, wants_loss);
+        } else {
+            // V need not be a multiple of 8, nor the row padded: the logits
+            // behind the last whole vector go to one thread each
+            if (tid < ntail) {
+                const __nv_bfloat16 zt = z[8 * nfull + tid];
+                reinterpret_cast<__nv_bfloat16*>(slice)[8 * nfull + tid] = zt;
+                xt = ds_arg<CAP>(a, a.flip ? -__bfloat162float(zt) : __bfloat162float(zt));
+                m = fmaxf(m, xt);
+                s = ds_rel<CAP>(xt, m, a.k);
+            }
+            // The slice's maximum and sum.  A batch's maximum comes first, so
+            // that the running sum is rescaled at most once a batch.
 #pragma unroll
-        for (int g = 0; g < kDsParts; ++g) {
-            if (g == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
-            if (g == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
-            if (g == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-            if (g == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
-            for (int i = 0; i < part; i += kDsBatch) {
-                const int j0 = tid + (g * part + i) * T;
+            for (int g = 0; g < kDsParts; ++g) {
+                if (g == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
+                if (g == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
+                if (g == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                if (g == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
                 const int stop = min(nfull, tid + (g + 1) * part * T);  // of this part
-                uint4 v[kDsBatch];
-                uint32_t m2 = 0xFF7FFF7Fu;  // two of bf16's lowest
+                for (int j0 = tid + g * part * T; j0 < stop; j0 += kDsBatch * T) {
+                    uint4 v[kDsBatch];
+                    uint32_t m2 = 0xFF7FFF7Fu;  // two of bf16's lowest
 #pragma unroll
-                for (int b = 0; b < kDsBatch; ++b) {
-                    if (j0 + b * T >= stop) break;
-                    v[b] = ds_signed(a, slice[j0 + b * T]);
-                    ds_max(m2, v[b]);
-                }
-                if (j0 >= stop) break;
-                const float mb = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xFFFF0000u));
-                const float xb = ds_arg<CAP>(a, mb);
-                if (xb > m) {
-                    s *= ds_ex2((m - xb) * a.k);
-                    m = xb;
-                }
-                const uint64_t mm = f2_packf(m, m);
-#pragma unroll
-                for (int b = 0; b < kDsBatch; ++b) {
-                    if (j0 + b * T >= stop) break;
-                    float x[8];
-                    ds_args8<CAP>(a, v[b], x);
-                    uint64_t e[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float lo, hi;
-                        f2_unpack(f2_mul(f2_sub(f2_packf(x[2 * q], x[2 * q + 1]), mm), kk), lo, hi);
-                        e[q] = f2_packf(ds_ex2(lo), ds_ex2(hi));
+                    for (int b = 0; b < kDsBatch; ++b) {
+                        if (j0 + b * T >= stop) break;
+                        v[b] = ds_signed(a, slice[j0 + b * T]);
+                        ds_max(m2, v[b]);
                     }
-                    float lo, hi;
-                    f2_unpack(f2_add(f2_add(e[0], e[1]), f2_add(e[2], e[3])), lo, hi);
-                    s += lo + hi;
+                    const float xb = ds_arg<CAP>(a, fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xFFFF0000u)));
+                    if (xb > m) {
+                        s *= ds_shift<CAP>(m, xb, a.k);
+                        m = xb;
+                    }
+                    s += ds_far<CAP>(m, a.k) ? ds_batch_sum<CAP, true>(a, v, j0, stop, m)
+                                             : ds_batch_sum<CAP, false>(a, v, j0, stop, m);
                 }
             }
         }
-        if (tid < ntail) {
-            const float M = fmaxf(m, xt);
-            s = s * ds_ex2((m - M) * a.k) + ds_ex2((xt - M) * a.k);
-            m = M;
-        }
         float M = ds_warp_max(m);
-        s = ds_warp_sum(s * ds_ex2((m - M) * a.k));
+        s = ds_warp_sum(s * ds_shift<CAP>(m, M, a.k));
         if (lane == 0) sh.warp[warp] = make_float2(M, s);
         __syncthreads();
         ds_cluster_wait();  // every block of the cluster runs: its shared memory may be written
         if (warp == 0) {
-            const float2 w = lane < T / 32 ? sh.warp[lane] : make_float2(CAP ? -1.0f : kDsLowest, 0.0f);
+            const float2 w = lane <= T / 32 ? sh.warp[lane] : make_float2(CAP ? -1.0f : kDsLowest, 0.0f);
             M = ds_warp_max(w.x);
-            s = ds_warp_sum(w.y * ds_ex2((w.x - M) * a.k));
+            s = ds_warp_sum(w.y * ds_shift<CAP>(w.x, M, a.k));
             if (lane < static_cast<int>(cluster)) {
                 uint32_t to;
                 const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(&sh.all[rank]));
@@ -351,17 +394,20 @@ __global__ void __launch_bounds__(kDsMaxThreads, 3) distill_kernel(const DsArgs 
         m = sh.all[0].x;
         for (uint32_t r = 1; r < cluster; ++r) m = fmaxf(m, sh.all[r].x);
         s = 0.0f;
-        for (uint32_t r = 0; r < cluster; ++r) s += sh.all[r].y * ds_ex2((sh.all[r].x - m) * a.k);
+        for (uint32_t r = 0; r < cluster; ++r) s += sh.all[r].y * ds_shift<CAP>(sh.all[r].x, m, a.k);
 
         wait_prior();  // the factor may come from the kernel before
-        const bool live = sh.live != 0;
-        if (warp == 0) {
+        const bool live = sh.live != 0, far = ds_far<CAP>(m, a.k);
+        zeros = !live;
+        if (teaches) {
             if (wants_loss) {
                 const float log_s = logf(s), inv_psum = sh.inv_psum;
+                constexpr float kLn2 = 0.6931471805599453f;
                 float sum = 0.0f;
                 for (int i = lane; i < a.K; i += 32) {
                     const float p = t.tp[i] * inv_psum;
-                    if (p != 0.0f) sum += p * ((t.tl[i] - t.log_psum) - ((t.tx[i] - m) * a.kn - log_s));
+                    const float x = far ? (t.tx[i] - m) * a.k : fmaf(t.tx[i], a.k, -__fmul_rn(m, a.k));
+                    if (p != 0.0f) sum += p * ((t.tl[i] - t.log_psum) - (x * kLn2 - log_s));
                 }
                 sum = ds_warp_sum(sum);
                 if (lane == 0)
@@ -369,48 +415,39 @@ __global__ void __launch_bounds__(kDsMaxThreads, 3) distill_kernel(const DsArgs 
             }
             if (t.bad && rank == 0 && lane == 0) atomicExch(a.status, -1);
         }
-        if (GRAD && !live) {
-            for (int j = tid; j < nfull; j += T) reinterpret_cast<uint4*>(dz)[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (tid < ntail) dz[8 * nfull + tid] = __float2bfloat16(0.0f);
-        }
         if (GRAD && live) {
             float g = a.T * (a.flip ? -a.scale : a.scale);
             if (a.dloss != nullptr) g *= a.dloss[row * a.dloss_stride];
             if (a.factor != nullptr) g *= a.factor[1];
-            const float gs = g / s;
-            const uint64_t mm = f2_packf(m, m), gg = f2_packf(CAP ? -4.0f * gs : gs, CAP ? -4.0f * gs : gs);
-#pragma unroll 2
-            for (int j = tid; j < nfull; j += T) {
-                float x[8], d[8];
-                ds_args8<CAP>(a, ds_signed(a, slice[j]), x);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint64_t x2 = f2_packf(x[2 * q], x[2 * q + 1]);
-                    float lo, hi;
-                    f2_unpack(f2_mul(f2_sub(x2, mm), kk), lo, hi);
-                    uint64_t d2 = f2_mul(f2_packf(ds_ex2(lo), ds_ex2(hi)), gg);
-                    if (CAP) d2 = f2_mul(d2, f2_fma(x2, x2, x2));  // 4 r (1 - r) = -4 (x^2 + x)
-                    f2_unpack(d2, d[2 * q], d[2 * q + 1]);
-                }
-                __stcs(reinterpret_cast<uint4*>(dz) + j, round8(d));
+            if (!teaches) {
+                if (far)
+                    ds_grad<CAP, true>(a, slice, reinterpret_cast<uint4*>(dz), nfull, m, g / s);
+                else
+                    ds_grad<CAP, false>(a, slice, reinterpret_cast<uint4*>(dz), nfull, m, g / s);
             }
             const auto one = [&](float x, float p) {
-                const float d = (ds_ex2((x - m) * a.k) / s - p) * g;
+                const float d = (ds_rel<CAP>(x, m, a.k) / s - p) * g;
                 return __float2bfloat16(CAP ? -4.0f * d * fmaf(x, x, x) : d);
             };
             if (tid < ntail) dz[8 * nfull + tid] = one(xt, 0.0f);
             __syncthreads();  // the teacher's elements are written a second time
             const float inv_psum = sh.inv_psum;
-            for (int i = tid; i < a.K; i += T) {
+            for (int i = tid; i < a.K; i += T + 32) {
                 const int c = t.tc[i];
                 const long long at = c - c0;
                 if (c < 0 || at < 0 || at >= n) continue;
                 bool first = true;  // the first entry of an id writes for all of them
                 float p = 0.0f;
-                for (int o = 0; o < a.K; ++o) {
-                    if (t.tc[o] != c) continue;
-                    first = first && o >= i;
-                    p += t.tp[o] * inv_psum;
+                for (int o = 0; o < a.Kp; o += 4) {
+                    const int4 q = *reinterpret_cast<const int4*>(t.tc + o);
+                    if (q.x != c && q.y != c && q.z != c && q.w != c) continue;
+                    const int is[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (is[e] == c) {
+                            first = first && o + e >= i;
+                            p += t.tp[o + e] * inv_psum;
+                        }
                 }
                 if (!first) continue;
                 const float zc = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(slice)[at]);
@@ -418,7 +455,12 @@ __global__ void __launch_bounds__(kDsMaxThreads, 3) distill_kernel(const DsArgs 
             }
         }
     }
+    if (GRAD && zeros) {
+        for (int j = tid; j < nfull; j += T + 32) reinterpret_cast<uint4*>(dz)[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (tid < ntail) dz[8 * nfull + tid] = __float2bfloat16(0.0f);
+    }
     if (a.out == nullptr || rank != 0) return;
+    __syncthreads();  // this row's loss is written
     if (tid == 0) {
         __threadfence();
         sh.last = atomicAdd(a.counter, 1u) == static_cast<uint32_t>(a.N - 1);

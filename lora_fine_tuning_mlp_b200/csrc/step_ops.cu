@@ -564,6 +564,7 @@ DsArgs ds_args(const lora_distill_shape* sh, const void* logits, const void* val
     a.V = sh->V;
     a.N = sh->N;
     a.K = static_cast<int>(sh->K);
+    a.Kp = (a.K + 3) / 4 * 4;
     a.values = values;
     a.ids = ids;
     a.values_f32 = sh->values_type == LORA_DISTILL_VALUES_FP32;
@@ -578,7 +579,6 @@ DsArgs ds_args(const lora_distill_shape* sh, const void* logits, const void* val
     constexpr double kLog2e = 1.4426950408889634;
     const double kn = (sh->softcap > 0.0f ? 2.0 * sh->softcap : std::fabs(static_cast<double>(sh->logit_scale))) /
                       sh->temperature;
-    a.kn = static_cast<float>(kn);
     a.k = static_cast<float>(kn * kLog2e);
     if (sh->softcap > 0.0f) a.cap2 = static_cast<float>(2.0 * a.scale / sh->softcap * kLog2e);
     a.status = status;
@@ -596,14 +596,16 @@ int launch_distill(const char* name, DsArgs a, int sms, cudaStream_t st, bool af
            (slice(a.log_cluster) > 32768 || ((a.N << a.log_cluster) * 2 <= sms && slice(a.log_cluster) > 4096)))
         ++a.log_cluster;
     a.slice = static_cast<int>(slice(a.log_cluster));
-    const int threads = std::min(kDsMaxThreads, std::max(64, a.slice / 8 / 4 / 32 * 32));
-    const size_t smem = std::max(static_cast<size_t>(a.slice) * 2 + static_cast<size_t>(a.K) * kDsEntryBytes,
+    a.threads = std::min(kDsMaxThreads, std::max(64, a.slice / 8 / 4 / 32 * 32));
+    const int threads = a.threads + 32;
+    const size_t smem = std::max(static_cast<size_t>(a.slice) * 2 + static_cast<size_t>(a.Kp) * kDsEntryBytes,
                                  static_cast<size_t>(threads) * 12);  // 12: the reduction's sums and counts
     const bool grad = a.dz != nullptr, cap = a.cap > 0.0f;
     auto kernel = grad ? (cap ? distill_kernel<true, true> : distill_kernel<true, false>)
                        : (cap ? distill_kernel<false, true> : distill_kernel<false, false>);
     STEP_TRY(allow_smem(kernel, kDsMaxV / kDsMaxCluster * 2 + kDsMaxK * kDsEntryBytes));
-    return launch(name, kernel, dim3(static_cast<unsigned>(a.N << a.log_cluster)), threads, smem, st, after_own,
+    return launch(name, kernel, dim3(static_cast<unsigned>(a.N << a.log_cluster)), dim3(static_cast<unsigned>(threads)),
+                  smem, st, after_own,
                   1 << a.log_cluster, a);
 }
 
