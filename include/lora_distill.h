@@ -25,7 +25,7 @@
  * (ld >= V, a multiple of 8), 16-byte aligned; the teacher's values [N, K] are
  * bf16 or fp32 and its ids [N, K] int32 or int64, densely packed, aligned to
  * their own size; labels int64 [N]; loss and dloss fp32 [N].  N, V, K >= 1,
- * V <= 851968, K <= 1024.  A row of logits is read once and stays in the
+ * V <= 753664, K <= 1024.  A row of logits is read once and stays in the
  * shared memory of a thread-block cluster, so loss and gradient together move
  * 4 bytes a logit; dlogits may be the logits buffer itself.  Other
  * conventions: lora_step.h.

@@ -9,12 +9,16 @@
 // on the chip: a cluster of 1, 2, 4 or 8 blocks holds it in shared memory as
 // the bf16 it came in, a slice each, the blocks exchange their (maximum, sum)
 // through distributed shared memory, and the gradient is formed from the
-// resident slice: 2 bytes a logit in, 2 out, nothing else.  Several blocks to
-// a multiprocessor overlap one's loads with another's arithmetic.
+// resident slice: 2 bytes a logit in, 2 out, nothing else.
 //
-// Every thread copies the 16-byte vectors that it later reads (cp.async), so
-// the loads need no barrier, and takes them up in four parts as they arrive;
-// one warp beside them takes the teacher's softmax.  Exponents are in base 2
+// Clusters stay and take row after row, about three blocks to a multiprocessor
+// so that one's exchange falls into another's arithmetic.  Every thread copies
+// the 16-byte vectors that it later reads (cp.async), so the loads need no
+// barrier: it takes them up in four parts as they arrive, and asks for the next
+// row's part as soon as it has used this row's for the last time.  A warp of
+// its own takes the teacher's softmax and the loss, and corrects the gradient
+// at the teacher's entries when the others are through with the row and on
+// their way into the next.  Exponents are in base 2
 // and relative to fl(m k) for the maximum m: fma(z, k, -fl(m k)) rounds once,
 // and sums relative to that very number are exact in it.  Where m k is out of
 // fma's range (rows filled with bf16's lowest value, say) the difference z - m
@@ -32,12 +36,12 @@
 namespace lmlp {
 namespace step {
 
-constexpr int kDsMaxThreads = 256;  // that work on the slice; a warp for the teacher comes on top
+constexpr int kDsMaxThreads = 256, kDsMinThreads = 64;  // that work on the slice; a warp for the teacher on top
 constexpr int kDsMaxCluster = 8;
 constexpr int kDsMaxK = 1024;
 constexpr int kDsParts = 4;   // of a thread's vectors, waited for one after the other
 constexpr int kDsBatch = 4;   // vectors taken up together
-constexpr int kDsEntryBytes = 16;  // of shared memory for a teacher's entry
+constexpr int kDsEntryBytes = 32;  // of shared memory for a teacher's entry, two rows' in turn; 4 for each place of the table of ids
 constexpr float kDsLowest = -3.3895313892515355e38f;  // bf16's lowest finite value
 
 struct DsArgs {
@@ -52,16 +56,15 @@ struct DsArgs {
     const long long* labels;  // may be null
     long long ignore;
     float inv_T, T;
-    float scale, cap;     // s with its sign taken off (see flip), cap or 0
-    uint32_t flip;        // 0x80008000 where s is negative: z and dz change sign
+    float scale, cap;     // s, cap or 0
+    float sign;           // of s: the largest exponent is that of the largest sign * z
     float k;              // base-2 exponent of a unit of z: s log2(e) / T; of a unit of -r: 2 cap log2(e) / T
     float cap2;           // 2 s / cap * log2(e)
     float* loss;          // may be null
     float* out;           // the reduced loss, or null
-    uint32_t* counter;    // rows done, zero before the launch (with out)
+    uint32_t* counter;    // clusters done, zero before the launch (with out)
     int mean;
-    int threads;          // that work on the slice
-    int Kp;               // K rounded up to 4
+    int log_table;        // places of the table of a row's ids: at least 2 K
     const float* dloss;   // [N], stride 0 or 1 (null: 1)
     long long dloss_stride;
     const float* factor;  // factor[1] multiplies it (null: 1)
@@ -126,81 +129,88 @@ __device__ __forceinline__ float ds_warp_sum(float v) {
     return v;
 }
 
-// The vector with its signs as the scale's magnitude wants them.
-__device__ __forceinline__ uint4 ds_signed(const DsArgs& a, uint4 v) {
-    if (a.flip) v = make_uint4(v.x ^ a.flip, v.y ^ a.flip, v.z ^ a.flip, v.w ^ a.flip);
-    return v;
-}
-__device__ __forceinline__ void ds_max(uint32_t& m2, const uint4& v) {
-    asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v.x));
-    asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v.y));
-    asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v.z));
-    asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(v.w));
-}
-
-// Whether m k is out of the range in which z k - fl(m k) is formed by one fma.
+// Maxima m are kept as sign * z (as -r with softcapping), so that more is more
+// whatever the sign of k; |k| m is their exponent.
 template <bool CAP>
-__device__ __forceinline__ bool ds_far(float m, float k) {
-    return !CAP && !(fabsf(m * k) < 1.0e30f);
+__device__ __forceinline__ float ds_exponent(const DsArgs& a, float m) {
+    return __fmul_rn(m, fabsf(a.k));
+}
+// Whether it is out of the range in which x k - fl(|k| m) is formed by one fma.
+template <bool CAP>
+__device__ __forceinline__ bool ds_far(const DsArgs& a, float m) {
+    return !CAP && !(fabsf(ds_exponent<CAP>(a, m)) < 1.0e30f);
 }
 // A term of a sum that is relative to m.
 template <bool CAP>
-__device__ __forceinline__ float ds_rel(float x, float m, float k) {
-    return ds_far<CAP>(m, k) ? ds_ex2((x - m) * k) : ds_ex2(fmaf(x, k, -__fmul_rn(m, k)));
+__device__ __forceinline__ float ds_rel(const DsArgs& a, float x, float m) {
+    return ds_far<CAP>(a, m) ? ds_ex2((x - a.sign * m) * a.k) : ds_ex2(fmaf(x, a.k, -ds_exponent<CAP>(a, m)));
 }
-// What turns a sum relative to m into one relative to M >= m: 2^(fl(m k) -
-// fl(M k)), both products rounded (1 where m = M).
+// What turns a sum relative to m into one relative to M >= m: 2 to the
+// difference of their exponents, both rounded (1 where m = M).
 template <bool CAP>
-__device__ __forceinline__ float ds_shift(float m, float M, float k) {
-    return ds_far<CAP>(M, k) ? ds_ex2((m - M) * k) : ds_ex2(__fmul_rn(m, k) - __fmul_rn(M, k));
+__device__ __forceinline__ float ds_shift(const DsArgs& a, float m, float M) {
+    return ds_far<CAP>(a, M) ? ds_ex2((m - M) * fabsf(a.k))
+                             : ds_ex2(ds_exponent<CAP>(a, m) - ds_exponent<CAP>(a, M));
 }
 
+constexpr int kDsMaxWarps = kDsMaxThreads / 32;
 struct DsShared {
-    float2 warp[32];            // (max, sum) of each warp
-    float2 all[kDsMaxCluster];  // ... of each block of the cluster, written by all of them
-    float inv_psum;             // teacher: 1 / sum of exp((a - max) / T)
-    int live;                   // it has an entry that counts
-    int last;                   // this block reduces the rows' losses
+    // (max, sum) of every warp of the cluster, written by all its blocks; the
+    // next row's go to the other half, so that a block may still read this one's
+    float2 all[2][kDsMaxCluster * kDsMaxWarps];
+    int live[2];  // the teacher has an entry that counts in this row
+    int last;     // this block reduces the rows' losses
 };
 
-// The teacher's entries of the row, by one warp: ids to tc, exp((a - max) / T)
-// to tp, its exponent to tl, and for the loss (`student`) what the student's
-// exponents are taken of at them to tx.
+// The teacher's entries of a row, in one warp's hands: ids to tc, exp((a -
+// max) / T) to tp, its exponent to tl, and to tx what the student's exponents
+// are taken of at the ids of this block's slice, for the loss (`all`) at every
+// id.
 struct DsTeacher {
     float *tp, *tl, *tx;
-    int* tc;
-    float log_psum;
-    bool bad;
+    int *tc, *table;
+    float inv_psum, log_psum;
+    bool bad, live, twice;  // twice: an id stands more than once
 };
 
 template <bool CAP>
-__device__ __forceinline__ void ds_teacher(const DsArgs& a, DsShared& sh, DsTeacher& t, long long row, bool student) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void ds_teacher(const DsArgs& a, DsTeacher& t, long long row, long long c0, int n, bool all) {
+    const int lane = threadIdx.x & 31, places = 1 << a.log_table;
+    for (int i = lane; i < places; i += 32) t.table[i] = -1;
+    __syncwarp();
     float amax = -3.4028234663852886e38f;  // fp32's lowest, which a teacher's mask may hold
-    bool any = false, bad = false;
-#pragma unroll 4
-    for (int i = lane; i < a.Kp; i += 32) {
-        const long long at = row * a.K + min(i, a.K - 1);
+    bool any = false, bad = false, twice = false;
+#pragma unroll 2
+    for (int i = lane; i < a.K; i += 32) {
+        const long long at = row * a.K + i;
         const long long id = a.ids_i64 ? static_cast<const long long*>(a.ids)[at] : static_cast<const int*>(a.ids)[at];
         const float v = a.values_f32 ? static_cast<const float*>(a.values)[at]
                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.values)[at]);
-        const bool in = i < a.K && id >= 0 && id < a.V;
+        const bool in = id >= 0 && id < a.V;
         bad = bad || id < -1 || id >= a.V;
         t.tc[i] = in ? static_cast<int>(id) : -1;
         t.tl[i] = v;
         if (in) {
             amax = fmaxf(amax, v);
             any = any || !(v == -INFINITY);
-            if (student) {
-                float z = __bfloat162float(a.z[row * a.ld + id]);
-                if (a.flip) z = -z;
+            if (all || (id >= c0 && id < c0 + n)) {
+                const float z = __bfloat162float(a.z[row * a.ld + id]);
                 t.tx[i] = CAP ? -1.0f / (1.0f + expf(2.0f * (a.scale / a.cap * z))) : z;
+            }
+            // at most K ids for at least 2 K places: a free one is found
+            const int c = static_cast<int>(id);
+            int at_table = static_cast<int>((static_cast<uint32_t>(c) * 2654435769u) >> (32 - a.log_table));
+            for (int tries = 0; tries < places; ++tries) {
+                const int seen = atomicCAS(t.table + at_table, -1, c);
+                twice = twice || seen == c;
+                if (seen == -1 || seen == c) break;
+                at_table = (at_table + 1) & (places - 1);
             }
         }
     }
     amax = ds_warp_max(amax);
     float psum = 0.0f;
-    for (int i = lane; i < a.Kp; i += 32) {
+    for (int i = lane; i < a.K; i += 32) {
         const float l = (t.tl[i] - amax) * a.inv_T, e = t.tc[i] >= 0 ? expf(l) : 0.0f;
         t.tl[i] = l;
         t.tp[i] = e;
@@ -208,23 +218,47 @@ __device__ __forceinline__ void ds_teacher(const DsArgs& a, DsShared& sh, DsTeac
     }
     psum = ds_warp_sum(psum);
     t.log_psum = logf(psum);
+    t.inv_psum = 1.0f / psum;
     t.bad = __any_sync(0xffffffffu, bad);
-    any = __any_sync(0xffffffffu, any);
-    if (lane == 0) {
-        sh.inv_psum = 1.0f / psum;
-        sh.live = any;
-    }
+    t.live = __any_sync(0xffffffffu, any);
+    t.twice = __any_sync(0xffffffffu, twice);
+    __syncwarp();
 }
 
-// A batch's exponentials added up: sum of 2^(x k - m k) over the vectors j0, j0
-// + T, ... below `stop`.
+// The largest sign * z of the first `count` of a batch's vectors.
+__device__ __forceinline__ float ds_batch_max(const DsArgs& a, const uint4 (&v)[kDsBatch], int count) {
+    uint32_t m2;
+    if (a.sign > 0.0f) {
+        m2 = 0xFF7FFF7Fu;  // two of bf16's lowest
+#pragma unroll
+        for (int b = 0; b < kDsBatch; ++b) {
+            if (b >= count) break;
+            const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w[i]));
+        }
+        return fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xFFFF0000u));
+    }
+    m2 = 0x7F7F7F7Fu;  // two of its largest
+#pragma unroll
+    for (int b = 0; b < kDsBatch; ++b) {
+        if (b >= count) break;
+        const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("min.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w[i]));
+    }
+    return -fminf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xFFFF0000u));
+}
+
+// The exponentials of the first `count` of a batch's vectors added up,
+// relative to m.
 template <bool CAP, bool FAR>
-__device__ __forceinline__ float ds_batch_sum(const DsArgs& a, const uint4 (&v)[kDsBatch], int j0, int stop, float m) {
-    const float c = FAR ? m : -__fmul_rn(m, a.k);
+__device__ __forceinline__ float ds_batch_sum(const DsArgs& a, const uint4 (&v)[kDsBatch], int count, float m) {
+    const float c = FAR ? a.sign * m : -ds_exponent<CAP>(a, m);
     float s = 0.0f;
 #pragma unroll
     for (int b = 0; b < kDsBatch; ++b) {
-        if (j0 + b * a.threads >= stop) break;
+        if (b >= count) break;
         float x[8];
         ds_args8<CAP>(a, v[b], x);
 #pragma unroll
@@ -234,30 +268,32 @@ __device__ __forceinline__ float ds_batch_sum(const DsArgs& a, const uint4 (&v)[
     return s;
 }
 
-// The gradient of the whole vectors, the teacher's part left out: gs 2^(x k -
-// m k) dt/dz.  The factor gs goes into the exponent (its sign apart): it is
-// off by 2^-24 of that exponent, far below the rounding to bf16.
-template <bool CAP, bool FAR>
-__device__ __forceinline__ void ds_grad(const DsArgs& a, const uint4* slice, uint4* dz, int nfull, float m, float gs) {
-    const float c = FAR ? m : log2f(fabsf(CAP ? 4.0f * gs : gs)) - __fmul_rn(m, a.k);
-    const uint32_t sign = !FAR && ((gs < 0.0f) != CAP) ? 0x80008000u : 0u;  // x^2 + x below is negative
-#pragma unroll 2
-    for (int j = threadIdx.x; j < nfull; j += a.threads) {
-        float x[8];
-        ds_args8<CAP>(a, ds_signed(a, slice[j]), x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (FAR) {
-                x[e] = ds_ex2((x[e] - c) * a.k) * gs;
-            } else {
-                const float y = ds_ex2(fmaf(x[e], a.k, c));
-                x[e] = CAP ? y * fmaf(x[e], x[e], x[e]) : y;  // r (1 - r) = -(x^2 + x)
-            }
-        }
-        uint4 o = round8(x);
-        if (sign) o = make_uint4(o.x ^ sign, o.y ^ sign, o.z ^ sign, o.w ^ sign);
-        __stcs(dz + j, o);
+// A batch taken into the running (m, s).  Its maximum comes first, so that the
+// sum is rescaled at most once a batch.
+template <bool CAP>
+__device__ __forceinline__ void ds_take(const DsArgs& a, const uint4 (&v)[kDsBatch], int count, float& m, float& s) {
+    float mb = ds_batch_max(a, v, count);
+    if (CAP) mb = ds_arg<CAP>(a, a.sign * mb);
+    if (mb > m) {
+        s *= ds_shift<CAP>(a, m, mb);
+        m = mb;
     }
+    s += ds_far<CAP>(a, m) ? ds_batch_sum<CAP, true>(a, v, count, m) : ds_batch_sum<CAP, false>(a, v, count, m);
+}
+
+// The gradient of a vector, the teacher's part left out: gs 2^(x k - |k| m)
+// dt/dz.  Where gs is positive it goes into the exponent: the result is off by
+// 2^-24 of that exponent, far below its rounding to bf16.
+template <bool CAP, bool PLAIN>
+__device__ __forceinline__ uint4 ds_grad8(const DsArgs& a, const uint4& v, float m, float c, float gs) {
+    float x[8];
+    ds_args8<CAP>(a, v, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float y = PLAIN ? ds_rel<CAP>(a, x[e], m) * gs : ds_ex2(fmaf(x[e], a.k, c));
+        x[e] = CAP ? y * fmaf(-x[e], x[e], -x[e]) : y;  // r (1 - r) = -x^2 - x
+    }
+    return round8(x);
 }
 
 // The rows' losses reduced by one block, in fp64 and a fixed order.
@@ -286,191 +322,236 @@ __device__ __forceinline__ void ds_reduce(const DsArgs& a, double* sum) {
     }
 }
 
-// One row a cluster.
-template <bool GRAD, bool CAP>
-__global__ void __launch_bounds__(kDsMaxThreads + 32, 3) distill_kernel(const DsArgs a) {
+// Waits for part g of the row at hand.  Behind it in the queue are the row's
+// other parts and, without a gradient, those of the next row asked for since:
+// three in all.
+template <bool GRAD>
+__device__ __forceinline__ void ds_wait_part(int g) {
+    if (!GRAD || g == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    if (GRAD && g == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    if (GRAD && g == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if (GRAD && g == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <bool GRAD, bool CAP, int T>
+__global__ void __launch_bounds__(T + 32, T == kDsMaxThreads ? 3 : 8) distill_kernel(const DsArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ DsShared sh;
     let_next();
-    const int T = a.threads, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int W = T / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool teaches = tid >= T;  // the last warp
     const uint32_t rank = ds_rank(), cluster = 1u << a.log_cluster;
-    const long long row = blockIdx.x >> a.log_cluster;
+    const long long stride = gridDim.x >> a.log_cluster;
     const long long c0 = static_cast<long long>(rank) * a.slice;
     const int n = static_cast<int>(max(0LL, min(static_cast<long long>(a.slice), a.V - c0)));  // this block's logits
     const int nfull = n >> 3, ntail = n & 7;
     const int part = (nfull + T * kDsParts - 1) / (T * kDsParts);  // a thread's vectors of a part
     uint4* slice = reinterpret_cast<uint4*>(raw);
-    const __nv_bfloat16* z = a.z + row * a.ld + c0;
-    if (!teaches) {
-        const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(slice));
-#pragma unroll
-        for (int g = 0; g < kDsParts; ++g) {
-            for (int i = 0; i < part; ++i) {
-                const int j = tid + (g * part + i) * T;
-                if (j < nfull)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sbase + 16u * j), "l"(z + 8 * j)
-                                 : "memory");
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+    const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(slice));
+    const bool wants_loss = rank == 0 && a.loss != nullptr;
+    const auto ignored = [&](long long row) { return a.labels != nullptr && row < a.N && a.labels[row] == a.ignore; };
+
+    // Part g of a row into this thread's places of the slice.
+    const auto ask = [&](int g, long long row) {
+        if (row < a.N) {
+            const __nv_bfloat16* z = a.z + row * a.ld + c0;
+            const int stop = min(nfull, (g + 1) * part * T);
+#pragma unroll 4
+            for (int j = tid + g * part * T; j < stop; j += T)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sbase + 16u * j), "l"(z + 8 * j)
+                             : "memory");
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const auto write_zeros = [&](long long row) {
+        __nv_bfloat16* dz = a.dz + row * a.ld + c0;
+        for (int j = tid; j < nfull; j += T) __stcs(reinterpret_cast<uint4*>(dz) + j, make_uint4(0u, 0u, 0u, 0u));
+        if (tid < ntail) dz[8 * nfull + tid] = __float2bfloat16(0.0f);
+    };
+    // The first row from `row` on that takes part; those passed over are
+    // finished here (labels are the same for the whole cluster).
+    const auto taking_part = [&](long long row, bool skip) {
+        while (skip) {
+            if (GRAD && !teaches) write_zeros(row);
+            if (wants_loss && tid == T) a.loss[row] = 0.0f;
+            row += stride;
+            skip = ignored(row);
+        }
+        return row;
+    };
+
+    long long row = blockIdx.x >> a.log_cluster;
+    row = taking_part(row, ignored(row));
+    if (!teaches) {
+#pragma unroll
+        for (int g = 0; g < kDsParts; ++g) ask(g, row);
     }
     ds_cluster_arrive();
-    const bool ignored = a.labels != nullptr && a.labels[row] == a.ignore;  // the same for the whole cluster
-    const bool wants_loss = rank == 0 && a.loss != nullptr;
-    __nv_bfloat16* dz = GRAD ? a.dz + row * a.ld + c0 : nullptr;
-    bool zeros = ignored;
-    if (ignored) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        wait_prior();
-        ds_cluster_wait();
-        if (wants_loss && tid == 0) a.loss[row] = 0.0f;
-    } else {
-        DsTeacher t{};
-        t.tp = reinterpret_cast<float*>(raw + static_cast<size_t>(a.slice) * 2);
-        t.tl = t.tp + a.Kp;
-        t.tx = t.tl + a.Kp;
-        t.tc = reinterpret_cast<int*>(t.tx + a.Kp);
+    // The teacher's warp prepares a row while the others write the gradient of
+    // the one before it.
+    DsTeacher t{}, ahead{};
+    const auto prepare = [&](DsTeacher& d, int turn, long long row) {
+        float* at = reinterpret_cast<float*>(raw + static_cast<size_t>(a.slice) * 2);
+        d.table = reinterpret_cast<int*>(at + 8 * a.K);
+        at += turn * 4 * a.K;
+        d.tp = at;
+        d.tl = at + a.K;
+        d.tx = at + 2 * a.K;
+        d.tc = reinterpret_cast<int*>(at + 3 * a.K);
+        ds_teacher<CAP>(a, d, row, c0, n, wants_loss);
+        if (lane == 0) sh.live[turn] = d.live;
+        __syncwarp();
+    };
+    if (teaches && row < a.N) prepare(t, 0, row);
+    const float up = a.T * a.scale;
+    ds_cluster_wait();  // every block of the cluster runs: its shared memory may be written
+    for (int turn = 0; row < a.N; turn ^= 1) {
+        const bool skip = ignored(row + stride);
+        long long next = GRAD ? 0 : taking_part(row + stride, skip);
         float m = CAP ? -1.0f : kDsLowest, s = 0.0f, xt = 0.0f;
-        if (teaches) {
-            ds_teacher<CAP>(a, sh, t, row, wants_loss);
-        } else {
+        if (!teaches) {
             // V need not be a multiple of 8, nor the row padded: the logits
             // behind the last whole vector go to one thread each
             if (tid < ntail) {
-                const __nv_bfloat16 zt = z[8 * nfull + tid];
-                reinterpret_cast<__nv_bfloat16*>(slice)[8 * nfull + tid] = zt;
-                xt = ds_arg<CAP>(a, a.flip ? -__bfloat162float(zt) : __bfloat162float(zt));
-                m = fmaxf(m, xt);
-                s = ds_rel<CAP>(xt, m, a.k);
+                const float zt = __bfloat162float(a.z[row * a.ld + c0 + 8 * nfull + tid]);
+                xt = ds_arg<CAP>(a, zt);
+                m = fmaxf(m, CAP ? xt : a.sign * xt);
+                s = ds_rel<CAP>(a, xt, m);
             }
-            // The slice's maximum and sum.  A batch's maximum comes first, so
-            // that the running sum is rescaled at most once a batch.
+            // the slice's maximum and sum
 #pragma unroll
             for (int g = 0; g < kDsParts; ++g) {
-                if (g == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
-                if (g == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
-                if (g == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-                if (g == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
-                const int stop = min(nfull, tid + (g + 1) * part * T);  // of this part
+                ds_wait_part<GRAD>(g);
+                const int stop = min(nfull, (g + 1) * part * T);
+#pragma unroll 1
                 for (int j0 = tid + g * part * T; j0 < stop; j0 += kDsBatch * T) {
                     uint4 v[kDsBatch];
-                    uint32_t m2 = 0xFF7FFF7Fu;  // two of bf16's lowest
+                    if (j0 + (kDsBatch - 1) * T < stop) {
 #pragma unroll
-                    for (int b = 0; b < kDsBatch; ++b) {
-                        if (j0 + b * T >= stop) break;
-                        v[b] = ds_signed(a, slice[j0 + b * T]);
-                        ds_max(m2, v[b]);
+                        for (int b = 0; b < kDsBatch; ++b) v[b] = slice[j0 + b * T];
+                        ds_take<CAP>(a, v, kDsBatch, m, s);
+                    } else {
+                        for (int j = j0; j < stop; j += T) {
+                            v[0] = slice[j];
+                            ds_take<CAP>(a, v, 1, m, s);
+                        }
                     }
-                    const float xb = ds_arg<CAP>(a, fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xFFFF0000u)));
-                    if (xb > m) {
-                        s *= ds_shift<CAP>(m, xb, a.k);
-                        m = xb;
-                    }
-                    s += ds_far<CAP>(m, a.k) ? ds_batch_sum<CAP, true>(a, v, j0, stop, m)
-                                             : ds_batch_sum<CAP, false>(a, v, j0, stop, m);
                 }
+                if (!GRAD) ask(g, next);
             }
-        }
-        float M = ds_warp_max(m);
-        s = ds_warp_sum(s * ds_shift<CAP>(m, M, a.k));
-        if (lane == 0) sh.warp[warp] = make_float2(M, s);
-        __syncthreads();
-        ds_cluster_wait();  // every block of the cluster runs: its shared memory may be written
-        if (warp == 0) {
-            const float2 w = lane <= T / 32 ? sh.warp[lane] : make_float2(CAP ? -1.0f : kDsLowest, 0.0f);
-            M = ds_warp_max(w.x);
-            s = ds_warp_sum(w.y * ds_shift<CAP>(w.x, M, a.k));
+            const float M = ds_warp_max(m);
+            s = ds_warp_sum(s * ds_shift<CAP>(a, m, M));
             if (lane < static_cast<int>(cluster)) {
                 uint32_t to;
-                const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(&sh.all[rank]));
+                const uint32_t mine =
+                    static_cast<uint32_t>(__cvta_generic_to_shared(&sh.all[turn][rank * W + warp]));
                 asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(lane));
                 asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(M), "f"(s) : "memory");
             }
-            __syncwarp();
         }
+        __syncwarp();
         ds_cluster_arrive();
         ds_cluster_wait();
-        m = sh.all[0].x;
-        for (uint32_t r = 1; r < cluster; ++r) m = fmaxf(m, sh.all[r].x);
-        s = 0.0f;
-        for (uint32_t r = 0; r < cluster; ++r) s += sh.all[r].y * ds_shift<CAP>(sh.all[r].x, m, a.k);
-
+        {
+            // each warp merges all warps' sums, in the same order everywhere
+            const int entries = static_cast<int>(cluster) * W;
+            const float2 none = make_float2(CAP ? -1.0f : kDsLowest, 0.0f);
+            const float2 w0 = lane < entries ? sh.all[turn][lane] : none;
+            const float2 w1 = lane + 32 < entries ? sh.all[turn][lane + 32] : none;
+            m = ds_warp_max(fmaxf(w0.x, w1.x));
+            s = ds_warp_sum(w0.y * ds_shift<CAP>(a, w0.x, m) + w1.y * ds_shift<CAP>(a, w1.x, m));
+        }
+        const bool live = sh.live[turn] != 0, far = ds_far<CAP>(a, m);
         wait_prior();  // the factor may come from the kernel before
-        const bool live = sh.live != 0, far = ds_far<CAP>(m, a.k);
-        zeros = !live;
-        if (teaches) {
+        float g = up;
+        if (GRAD) {
+            next = taking_part(row + stride, skip);
+            if (a.dloss != nullptr) g *= a.dloss[row * a.dloss_stride];
+            if (a.factor != nullptr) g *= a.factor[1];
+        }
+        __nv_bfloat16* dz = GRAD ? a.dz + row * a.ld + c0 : nullptr;
+        const auto one = [&](float x, float p) {
+            const float d = (ds_rel<CAP>(a, x, m) / s - p) * g;
+            return __float2bfloat16(CAP ? 4.0f * d * fmaf(-x, x, -x) : d);
+        };
+        if (!teaches) {
+            if (GRAD) {
+                if (tid < ntail) dz[8 * nfull + tid] = live ? one(xt, 0.0f) : __float2bfloat16(0.0f);
+                uint4* o = reinterpret_cast<uint4*>(dz);
+                const float gs = (CAP ? 4.0f : 1.0f) * (g / s);
+                const float c = log2f(gs) - ds_exponent<CAP>(a, m);
+#pragma unroll 1
+                for (int q = 0; q < kDsParts; ++q) {
+                    const int from = tid + q * part * T, stop = min(nfull, (q + 1) * part * T);
+                    if (live && !far && gs > 0.0f) {
+#pragma unroll 4
+                        for (int j = from; j < stop; j += T) __stcs(o + j, ds_grad8<CAP, false>(a, slice[j], m, c, gs));
+                    } else {
+                        for (int j = from; j < stop; j += T)
+                            __stcs(o + j, live ? ds_grad8<CAP, true>(a, slice[j], m, c, gs) : make_uint4(0u, 0u, 0u, 0u));
+                    }
+                    ask(q, next);
+                }
+                __syncwarp();
+                asm volatile("bar.arrive 1, %0;" ::"r"(T + 32) : "memory");
+            }
+        } else {
             if (wants_loss) {
-                const float log_s = logf(s), inv_psum = sh.inv_psum;
+                const float log_s = logf(s);
                 constexpr float kLn2 = 0.6931471805599453f;
                 float sum = 0.0f;
                 for (int i = lane; i < a.K; i += 32) {
-                    const float p = t.tp[i] * inv_psum;
-                    const float x = far ? (t.tx[i] - m) * a.k : fmaf(t.tx[i], a.k, -__fmul_rn(m, a.k));
-                    if (p != 0.0f) sum += p * ((t.tl[i] - t.log_psum) - (x * kLn2 - log_s));
+                    const float p = t.tp[i] * t.inv_psum;
+                    if (p == 0.0f || t.tc[i] < 0) continue;
+                    const float x = far ? (t.tx[i] - a.sign * m) * a.k
+                                        : fmaf(t.tx[i], a.k, -ds_exponent<CAP>(a, m));
+                    sum += p * ((t.tl[i] - t.log_psum) - (x * kLn2 - log_s));
                 }
                 sum = ds_warp_sum(sum);
                 if (lane == 0)
                     a.loss[row] = t.bad ? __int_as_float(0x7fc00000) : (live ? a.T * a.T * sum : 0.0f);
             }
             if (t.bad && rank == 0 && lane == 0) atomicExch(a.status, -1);
-        }
-        if (GRAD && live) {
-            float g = a.T * (a.flip ? -a.scale : a.scale);
-            if (a.dloss != nullptr) g *= a.dloss[row * a.dloss_stride];
-            if (a.factor != nullptr) g *= a.factor[1];
-            if (!teaches) {
-                if (far)
-                    ds_grad<CAP, true>(a, slice, reinterpret_cast<uint4*>(dz), nfull, m, g / s);
-                else
-                    ds_grad<CAP, false>(a, slice, reinterpret_cast<uint4*>(dz), nfull, m, g / s);
-            }
-            const auto one = [&](float x, float p) {
-                const float d = (ds_rel<CAP>(x, m, a.k) / s - p) * g;
-                return __float2bfloat16(CAP ? -4.0f * d * fmaf(x, x, x) : d);
-            };
-            if (tid < ntail) dz[8 * nfull + tid] = one(xt, 0.0f);
-            __syncthreads();  // the teacher's elements are written a second time
-            const float inv_psum = sh.inv_psum;
-            for (int i = tid; i < a.K; i += T + 32) {
-                const int c = t.tc[i];
-                const long long at = c - c0;
-                if (c < 0 || at < 0 || at >= n) continue;
-                bool first = true;  // the first entry of an id writes for all of them
-                float p = 0.0f;
-                for (int o = 0; o < a.Kp; o += 4) {
-                    const int4 q = *reinterpret_cast<const int4*>(t.tc + o);
-                    if (q.x != c && q.y != c && q.z != c && q.w != c) continue;
-                    const int is[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (is[e] == c) {
-                            first = first && o + e >= i;
-                            p += t.tp[o + e] * inv_psum;
+            if (next < a.N) prepare(ahead, turn ^ 1, next);
+            if (GRAD) {
+                asm volatile("bar.sync 1, %0;" ::"r"(T + 32) : "memory");  // the row's gradient is written
+                for (int i = lane; live && i < a.K; i += 32) {
+                    const int c = t.tc[i];
+                    const long long at = c - c0;
+                    if (c < 0 || at < 0 || at >= n) continue;
+                    float p = t.tp[i];
+                    if (t.twice) {  // the first entry of an id writes for all of them
+                        bool first = true;
+                        p = 0.0f;
+                        for (int o = 0; o < a.K; ++o) {
+                            if (t.tc[o] != c) continue;
+                            first = first && o >= i;
+                            p += t.tp[o];
                         }
+                        if (!first) continue;
+                    }
+                    dz[at] = one(t.tx[i], p * t.inv_psum);
                 }
-                if (!first) continue;
-                const float zc = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(slice)[at]);
-                dz[at] = one(ds_arg<CAP>(a, a.flip ? -zc : zc), p);
+                __syncwarp();
             }
+            t = ahead;
         }
+        row = next;
     }
-    if (GRAD && zeros) {
-        for (int j = tid; j < nfull; j += T + 32) reinterpret_cast<uint4*>(dz)[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (tid < ntail) dz[8 * nfull + tid] = __float2bfloat16(0.0f);
-    }
+    wait_prior();  // in every block, whatever rows it had
     if (a.out == nullptr || rank != 0) return;
-    __syncthreads();  // this row's loss is written
+    __syncthreads();  // this block's losses are written
     if (tid == 0) {
         __threadfence();
-        sh.last = atomicAdd(a.counter, 1u) == static_cast<uint32_t>(a.N - 1);
+        sh.last = atomicAdd(a.counter, 1u) == static_cast<uint32_t>(stride - 1);
     }
     __syncthreads();
     if (sh.last) ds_reduce(a, reinterpret_cast<double*>(raw));
 }
 
 // out[1] = d out[0] / d loss of a row that takes part: 1 / (rows whose label
-// is not ignore_index) for the mean, else 1; and the counter of rows done.
+// is not ignore_index) for the mean, else 1; and the counter of clusters done.
 constexpr int kDsCountThreads = 1024;
 __global__ void __launch_bounds__(kDsCountThreads) distill_count_kernel(const long long* labels, long long N,
                                                                         long long ignore, int mean, float* out,

@@ -163,13 +163,57 @@ int launch(const char* name, void (*kernel)(P...), dim3 grid, dim3 block, size_t
     return LORA_MLP_OK;
 }
 
-// Raises a kernel's dynamic shared memory limit, once a device.
+// Raises a kernel's dynamic shared memory limit.
 template <class K>
 int allow_smem(K* kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) ==
                    cudaSuccess
                ? LORA_MLP_OK
                : LORA_MLP_ERR_CUDA;
+}
+
+// Clusters of a kernel that the current device holds at once.  CUDA takes
+// several microseconds to say; the last few answers are kept.
+struct Residency {
+    int dev;
+    const void* kernel;
+    int threads, cluster;
+    size_t smem;
+    int count;
+};
+constexpr int kResidencies = 16;
+Residency g_residency[kResidencies];
+int g_residency_next = 0;
+std::mutex g_residency_mu;
+
+template <class... P>
+int resident_clusters(void (*kernel)(P...), size_t max_smem, int threads, size_t smem, int cluster, int* count) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LORA_MLP_ERR_CUDA;
+    const void* key = reinterpret_cast<const void*>(kernel);
+    std::lock_guard<std::mutex> lk(g_residency_mu);
+    for (const Residency& r : g_residency)
+        if (r.kernel == key && r.dev == dev && r.threads == threads && r.cluster == cluster && r.smem == smem) {
+            *count = r.count;
+            return LORA_MLP_OK;
+        }
+    STEP_TRY(allow_smem(kernel, max_smem));
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {static_cast<unsigned>(cluster), 1u, 1u};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(count, kernel, &cfg) != cudaSuccess || *count < 1) {
+        cudaGetLastError();
+        return LORA_MLP_ERR_CUDA;
+    }
+    g_residency[g_residency_next] = {dev, key, threads, cluster, smem, *count};
+    g_residency_next = (g_residency_next + 1) % kResidencies;
+    return LORA_MLP_OK;
 }
 
 struct Carver {
@@ -539,7 +583,8 @@ int lora_qk_rope_backward(const lora_qk_shape* shape, const lora_qk_view* q, con
 
 namespace {
 
-constexpr int64_t kDsMaxV = int64_t{kDsMaxCluster} * 106496;  // 208 KB of shared memory a block
+constexpr int64_t kDsMaxV = int64_t{kDsMaxCluster} * 94208;  // 184 KB of shared memory a block
+constexpr size_t kDsMaxSmem = 2 * 94208 + kDsMaxK * (kDsEntryBytes + 2 * 4);
 
 int validate_distill(const lora_distill_shape* sh) {
     if (sh == nullptr) return LORA_MLP_ERR_INVALID_ARG;
@@ -564,7 +609,7 @@ DsArgs ds_args(const lora_distill_shape* sh, const void* logits, const void* val
     a.V = sh->V;
     a.N = sh->N;
     a.K = static_cast<int>(sh->K);
-    a.Kp = (a.K + 3) / 4 * 4;
+    a.log_table = std::max(5, ceil_log2(2 * static_cast<uint64_t>(a.K)));
     a.values = values;
     a.ids = ids;
     a.values_f32 = sh->values_type == LORA_DISTILL_VALUES_FP32;
@@ -573,12 +618,11 @@ DsArgs ds_args(const lora_distill_shape* sh, const void* logits, const void* val
     a.ignore = sh->ignore_index;
     a.T = sh->temperature;
     a.inv_T = 1.0f / sh->temperature;
-    a.scale = std::fabs(sh->logit_scale);
-    a.flip = sh->logit_scale < 0.0f ? 0x80008000u : 0u;
+    a.scale = sh->logit_scale;
+    a.sign = sh->logit_scale < 0.0f ? -1.0f : 1.0f;
     a.cap = sh->softcap;
     constexpr double kLog2e = 1.4426950408889634;
-    const double kn = (sh->softcap > 0.0f ? 2.0 * sh->softcap : std::fabs(static_cast<double>(sh->logit_scale))) /
-                      sh->temperature;
+    const double kn = (sh->softcap > 0.0f ? 2.0 * sh->softcap : 1.0 * sh->logit_scale) / sh->temperature;
     a.k = static_cast<float>(kn * kLog2e);
     if (sh->softcap > 0.0f) a.cap2 = static_cast<float>(2.0 * a.scale / sh->softcap * kLog2e);
     a.status = status;
@@ -596,17 +640,22 @@ int launch_distill(const char* name, DsArgs a, int sms, cudaStream_t st, bool af
            (slice(a.log_cluster) > 32768 || ((a.N << a.log_cluster) * 2 <= sms && slice(a.log_cluster) > 4096)))
         ++a.log_cluster;
     a.slice = static_cast<int>(slice(a.log_cluster));
-    a.threads = std::min(kDsMaxThreads, std::max(64, a.slice / 8 / 4 / 32 * 32));
-    const int threads = a.threads + 32;
-    const size_t smem = std::max(static_cast<size_t>(a.slice) * 2 + static_cast<size_t>(a.Kp) * kDsEntryBytes,
+    const bool wide = a.slice > 4096;  // below, a thread of a block of 256 would have fewer than two vectors
+    const int threads = (wide ? kDsMaxThreads : kDsMinThreads) + 32;
+    const size_t smem = std::max(static_cast<size_t>(a.slice) * 2 + static_cast<size_t>(a.K) * kDsEntryBytes +
+                                     (size_t{4} << a.log_table),
                                  static_cast<size_t>(threads) * 12);  // 12: the reduction's sums and counts
     const bool grad = a.dz != nullptr, cap = a.cap > 0.0f;
-    auto kernel = grad ? (cap ? distill_kernel<true, true> : distill_kernel<true, false>)
-                       : (cap ? distill_kernel<false, true> : distill_kernel<false, false>);
-    STEP_TRY(allow_smem(kernel, kDsMaxV / kDsMaxCluster * 2 + kDsMaxK * kDsEntryBytes));
-    return launch(name, kernel, dim3(static_cast<unsigned>(a.N << a.log_cluster)), dim3(static_cast<unsigned>(threads)),
-                  smem, st, after_own,
-                  1 << a.log_cluster, a);
+    auto kernel = wide ? (grad ? (cap ? distill_kernel<true, true, kDsMaxThreads> : distill_kernel<true, false, kDsMaxThreads>)
+                               : (cap ? distill_kernel<false, true, kDsMaxThreads> : distill_kernel<false, false, kDsMaxThreads>))
+                       : (grad ? (cap ? distill_kernel<true, true, kDsMinThreads> : distill_kernel<true, false, kDsMinThreads>)
+                               : (cap ? distill_kernel<false, true, kDsMinThreads> : distill_kernel<false, false, kDsMinThreads>));
+    // As many clusters as run at once; each takes every so many-th row.
+    int at_once = 0;
+    STEP_TRY(resident_clusters(kernel, kDsMaxSmem, threads, smem, 1 << a.log_cluster, &at_once));
+    const int64_t clusters = std::min<int64_t>(a.N, at_once);
+    return launch(name, kernel, dim3(static_cast<unsigned>(clusters << a.log_cluster)),
+                  dim3(static_cast<unsigned>(threads)), smem, st, after_own, 1 << a.log_cluster, a);
 }
 
 int check_distill(const lora_distill_shape* sh, const void* logits, const void* values, const void* ids,
