@@ -25,14 +25,16 @@
  * (ld >= V, a multiple of 8), 16-byte aligned; the teacher's values [N, K] are
  * bf16 or fp32 and its ids [N, K] int32 or int64, densely packed, aligned to
  * their own size; labels int64 [N]; loss and dloss fp32 [N].  N, V, K >= 1,
- * V <= 753664, K <= 1024.  A row of logits is read once and stays in the
+ * V <= 327680, K <= 1024.  A row of logits is read once and stays in the
  * shared memory of a thread-block cluster, so loss and gradient together move
- * 4 bytes a logit; dlogits may be the logits buffer itself.  Other
- * conventions: lora_step.h.
+ * 4 bytes a logit; dlogits may be the logits buffer itself.  The same call
+ * gives the same bits; a row's last bits may depend on the rows beside it.
+ * Other conventions: lora_step.h.
  *
  * A teacher id below -1 or not below V is a device-side finding: the entry
  * counts as absent, the row's loss is NaN, and lora_step_device_status reports
- * LORA_MLP_ERR_INVALID_ARG.
+ * LORA_MLP_ERR_INVALID_ARG.  LORA_MLP_ERR_DEVICE_TIMEOUT there means that a
+ * wait between blocks ran out (about 2 s) and the results are not complete.
  */
 #ifndef LORA_DISTILL_H
 #define LORA_DISTILL_H

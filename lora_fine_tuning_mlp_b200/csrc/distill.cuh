@@ -6,42 +6,49 @@
 //
 // The gradient needs the row's softmax sum before its first element, so a
 // kernel that streams rows from HBM has to read them twice.  Here a row stays
-// on the chip: a cluster of 1, 2, 4 or 8 blocks holds it in shared memory as
-// the bf16 it came in, a slice each, the blocks exchange their (maximum, sum)
-// through distributed shared memory, and the gradient is formed from the
-// resident slice: 2 bytes a logit in, 2 out, nothing else.
+// on the chip between its two passes: a cluster of 1, 2, 4 or 8 blocks holds
+// it in shared memory as the bf16 it came in, a slice each, and the gradient is
+// formed from the resident slice: 2 bytes a logit in, 2 out, nothing else.
 //
-// Clusters stay and take row after row, about three blocks to a multiprocessor
-// so that one's exchange falls into another's arithmetic.  Every thread copies
-// the 16-byte vectors that it later reads (cp.async), so the loads need no
-// barrier: it takes them up in four parts as they arrive, and asks for the next
-// row's part as soon as it has used this row's for the last time.  A warp of
-// its own takes the teacher's softmax and the loss, and corrects the gradient
-// at the teacher's entries when the others are through with the row and on
-// their way into the next.  Exponents are in base 2
-// and relative to fl(m k) for the maximum m: fma(z, k, -fl(m k)) rounds once,
-// and sums relative to that very number are exact in it.  Where m k is out of
-// fma's range (rows filled with bf16's lowest value, say) the difference z - m
-// is formed first.  With softcapping, t = cap tanh(s z / cap) = cap - 2 cap r
-// with r = 1 / (1 + 2^(cap2 z)): exponents are taken of -r, dt/dz = 4 s r (1 -
-// r) has no cancellation where tanh saturates, and four logits share one
-// reciprocal.
+// The clusters stay and take row after row as one stream of chunks (B vectors
+// for each thread) through a ring of shared memory.  In step k a thread adds
+// chunk k into its row's sum, turns chunk k - lag into gradient, and asks
+// (cp.async) for chunk k + kDsAhead in the place that this sets free.  It only
+// ever touches vectors of its own, so the ring needs no barrier.  The lag is a
+// row and one or two chunks: when a row's second pass begins, the sums that
+// its warps stored in all blocks of the cluster have arrived.  Three
+// more warps take the teacher's softmax and the loss, a row each in turn, and
+// correct the gradient at the teacher's entries once the row is written.
+//
+// One exponential a logit and pass is what the special-function unit can
+// deliver in about the time that HBM takes, so the passes do little else.  In
+// particular they look for no maximum: sums are taken relative to a reference
+// m that stays from row to row (0 at first), 2^(z k - m k) with one fma.  A row
+// whose sum leaves the middle of fp32's range (its largest logit far from m,
+// infinities, a vocabulary masked whole) is summed again, after a search for
+// its maximum, which is the reference from then on; where m k itself is out of
+// fma's range the difference z - m is formed first.  Either way the result is
+// the softmax to fp32's precision.  With softcapping, t = cap tanh(s z / cap)
+// = cap - 2 cap r with r = 1 / (1 + 2^(cap2 z)): exponents are taken of -r,
+// dt/dz = 4 s r (1 - r) has no cancellation where tanh saturates, and four
+// logits share one reciprocal.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
 
 #include "f32x2.cuh"
+#include "ptx.cuh"
 #include "vec8.cuh"
 
 namespace lmlp {
 namespace step {
 
-constexpr int kDsMaxThreads = 256, kDsMinThreads = 64;  // that work on the slice; a warp for the teacher on top
-constexpr int kDsMaxCluster = 8;
+constexpr int kDsAhead = 3;     // chunks asked for ahead of their first use
 constexpr int kDsMaxK = 1024;
-constexpr int kDsParts = 4;   // of a thread's vectors, waited for one after the other
-constexpr int kDsBatch = 4;   // vectors taken up together
-constexpr int kDsEntryBytes = 32;  // of shared memory for a teacher's entry, two rows' in turn; 4 for each place of the table of ids
+constexpr int kDsDepth = 8;     // rows under way (see DsShared)
+constexpr int kDsTeachers = 3;  // warps that take the teacher's part, a row each in turn
+constexpr int kDsTimeout = -7;  // LORA_MLP_ERR_DEVICE_TIMEOUT
+constexpr int kDsEntryBytes = 16;  // of shared memory for a teacher's entry, and 4 for each place of the table of ids
 constexpr float kDsLowest = -3.3895313892515355e38f;  // bf16's lowest finite value
 
 struct DsArgs {
@@ -51,6 +58,11 @@ struct DsArgs {
     int K;
     int slice;  // logits of a block: a multiple of 8
     int log_cluster;
+    int chunks;  // of a slice
+    int chunk;   // vectors of a chunk
+    int lag;     // chunks between a chunk's two uses
+    int slots;   // chunks of the ring
+    long long wait_limit;  // SM cycles that a wait may take before the kernel gives up
     const void *values, *ids;
     int values_f32, ids_i64;
     const long long* labels;  // may be null
@@ -129,38 +141,106 @@ __device__ __forceinline__ float ds_warp_sum(float v) {
     return v;
 }
 
-// Maxima m are kept as sign * z (as -r with softcapping), so that more is more
-// whatever the sign of k; |k| m is their exponent.
-template <bool CAP>
-__device__ __forceinline__ float ds_exponent(const DsArgs& a, float m) {
-    return __fmul_rn(m, fabsf(a.k));
-}
+// References m are kept as sign * z (as -r with softcapping), so that more is
+// more whatever the sign of k; |k| m is their exponent.
+__device__ __forceinline__ float ds_exponent(const DsArgs& a, float m) { return __fmul_rn(m, fabsf(a.k)); }
 // Whether it is out of the range in which x k - fl(|k| m) is formed by one fma.
 template <bool CAP>
 __device__ __forceinline__ bool ds_far(const DsArgs& a, float m) {
-    return !CAP && !(fabsf(ds_exponent<CAP>(a, m)) < 1.0e30f);
+    return !CAP && !(fabsf(ds_exponent(a, m)) < 1.0e30f);
 }
 // A term of a sum that is relative to m.
 template <bool CAP>
 __device__ __forceinline__ float ds_rel(const DsArgs& a, float x, float m) {
-    return ds_far<CAP>(a, m) ? ds_ex2((x - a.sign * m) * a.k) : ds_ex2(fmaf(x, a.k, -ds_exponent<CAP>(a, m)));
-}
-// What turns a sum relative to m into one relative to M >= m: 2 to the
-// difference of their exponents, both rounded (1 where m = M).
-template <bool CAP>
-__device__ __forceinline__ float ds_shift(const DsArgs& a, float m, float M) {
-    return ds_far<CAP>(a, M) ? ds_ex2((m - M) * fabsf(a.k))
-                             : ds_ex2(ds_exponent<CAP>(a, m) - ds_exponent<CAP>(a, M));
+    return ds_far<CAP>(a, m) ? ds_ex2((x - a.sign * m) * a.k) : ds_ex2(fmaf(x, a.k, -ds_exponent(a, m)));
 }
 
-constexpr int kDsMaxWarps = kDsMaxThreads / 32;
+// The warps of a cluster that work on its slices tell one another a number
+// each, in an 8-byte store to every block's shared memory together with a tag,
+// which is how the readers know it has come.  Sums of row i (i = 0, 1, ... of
+// the cluster's) have the tag i + 1 and buffer i mod kDsDepth, which is free
+// again in time: the lag is at most chunks + 1, or chunks + 2 where a slice has
+// two chunks or more, so a warp that sends row x's sum has received row x -
+// 3's, and the warps that sent those had received row x - 6's.  Exchanges for
+// rows that are summed again are counted by themselves and use two buffers in
+// turn: a warp that sends number f has received f - 1, sent by warps that had
+// received f - 2.
+//
+// A row's teacher sets `ready` when it has prepared the row, having finished
+// with row i - 3; block 0's sets `read` in all blocks.  The first warp tells it
+// the row's reference and sum in `told`.
 struct DsShared {
-    // (max, sum) of every warp of the cluster, written by all its blocks; the
-    // next row's go to the other half, so that a block may still read this one's
-    float2 all[2][kDsMaxCluster * kDsMaxWarps];
-    int live[2];  // the teacher has an entry that counts in this row
-    int last;     // this block reduces the rows' losses
+    float reference[kDsDepth];  // that row i's sums are relative to
+    int ready[kDsDepth];  // 2 (i + 1), + 1 where the teacher has an entry that counts
+    int read[kDsDepth];   // i + 1 when block 0's teacher reads the logits of row i no more
+    float told[kDsDepth][2];
+    int told_row[kDsDepth];       // i + 1
+    uint64_t done[kDsTeachers];   // mbarriers: a row's gradient is written
+    int gave_up;                  // a wait ran out
+    int last;                     // this block reduces the rows' losses
 };
+
+__device__ __forceinline__ uint32_t ds_smem(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ uint32_t ds_remote(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+template <class V>
+__device__ __forceinline__ V ds_look(const V* p) {
+    return *static_cast<const volatile V*>(p);
+}
+
+// Polls until `here` holds in every lane of the warp, for a limited time; false
+// where it ran out here or for another of the block's warps.
+template <class F>
+__device__ __forceinline__ bool ds_wait(const DsArgs& a, DsShared& sh, F here) {
+    if (__all_sync(0xffffffffu, here())) return true;
+    const long long begin = clock64();
+    for (;;) {
+        __nanosleep(300);  // polls without a pause take issue slots from the warps that work: 3 % of the kernel's time
+        if (__all_sync(0xffffffffu, here())) return true;
+        const bool stop = ds_look(&sh.gave_up) != 0 || clock64() - begin > a.wait_limit;
+        if (__any_sync(0xffffffffu, stop)) {
+            if (ds_look(&sh.gave_up) == 0) atomicExch(a.status, kDsTimeout);
+            *static_cast<volatile int*>(&sh.gave_up) = 1;
+            return false;
+        }
+    }
+}
+
+// Sends this warp's v as its cell (`mine`) of the buffer at `cell` to every block.
+__device__ __forceinline__ void ds_send(const uint64_t* cell, int mine, int cluster, uint32_t tag, float v) {
+    const int lane = threadIdx.x & 31;
+    __threadfence_block();  // the row's reference before the sum that its readers wait for
+    if (lane < cluster) {
+        const uint32_t to = ds_remote(ds_smem(cell + mine), static_cast<uint32_t>(lane));
+        asm volatile("st.volatile.shared::cluster.u64 [%0], %1;" ::"r"(to),
+                     "l"(static_cast<uint64_t>(tag) << 32 | __float_as_uint(v))
+                     : "memory");
+    }
+    __syncwarp();
+}
+// The sum, or the largest, of a buffer's cells, the same bits for every warp;
+// false where the wait ran out.
+template <bool MAX>
+__device__ __forceinline__ bool ds_receive(const DsArgs& a, DsShared& sh, const uint64_t* cell, int cells, uint32_t tag,
+                                           float& v) {
+    const int lane = threadIdx.x & 31;
+    if (!ds_wait(a, sh, [&] {
+            bool here = true;
+            for (int e = lane; e < cells; e += 32) here = here && static_cast<uint32_t>(ds_look(cell + e) >> 32) == tag;
+            return here;
+        }))
+        return false;
+    v = MAX ? -INFINITY : 0.0f;
+    for (int e = lane; e < cells; e += 32) {
+        const float c = __uint_as_float(static_cast<uint32_t>(ds_look(cell + e)));
+        v = MAX ? fmaxf(v, c) : v + c;
+    }
+    v = MAX ? ds_warp_max(v) : ds_warp_sum(v);
+    return true;
+}
 
 // The teacher's entries of a row, in one warp's hands: ids to tc, exp((a -
 // max) / T) to tp, its exponent to tl, and to tx what the student's exponents
@@ -225,76 +305,72 @@ __device__ __forceinline__ void ds_teacher(const DsArgs& a, DsTeacher& t, long l
     __syncwarp();
 }
 
-// The largest sign * z of the first `count` of a batch's vectors.
-__device__ __forceinline__ float ds_batch_max(const DsArgs& a, const uint4 (&v)[kDsBatch], int count) {
-    uint32_t m2;
-    if (a.sign > 0.0f) {
-        m2 = 0xFF7FFF7Fu;  // two of bf16's lowest
+// 2^(x k + c) of eight, added to acc two by two.
+__device__ __forceinline__ void ds_add8(const DsArgs& a, const float (&x)[8], float c, uint64_t& acc) {
+    const uint64_t kk = f2_packf(a.k, a.k), cc = f2_packf(c, c);
+    uint64_t e[4];
 #pragma unroll
-        for (int b = 0; b < kDsBatch; ++b) {
-            if (b >= count) break;
-            const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w[i]));
-        }
-        return fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xFFFF0000u));
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f2_unpack(f2_fma(f2_packf(x[2 * i], x[2 * i + 1]), kk, cc), lo, hi);
+        e[i] = f2_packf(ds_ex2(lo), ds_ex2(hi));
     }
-    m2 = 0x7F7F7F7Fu;  // two of its largest
-#pragma unroll
-    for (int b = 0; b < kDsBatch; ++b) {
-        if (b >= count) break;
-        const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) asm("min.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w[i]));
-    }
-    return -fminf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xFFFF0000u));
+    acc = f2_add(acc, f2_add(f2_add(e[0], e[1]), f2_add(e[2], e[3])));
 }
 
-// The exponentials of the first `count` of a batch's vectors added up,
-// relative to m.
-template <bool CAP, bool FAR>
-__device__ __forceinline__ float ds_batch_sum(const DsArgs& a, const uint4 (&v)[kDsBatch], int count, float m) {
-    const float c = FAR ? a.sign * m : -ds_exponent<CAP>(a, m);
-    float s = 0.0f;
-#pragma unroll
-    for (int b = 0; b < kDsBatch; ++b) {
-        if (b >= count) break;
-        float x[8];
-        ds_args8<CAP>(a, v[b], x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = ds_ex2(FAR ? (x[e] - c) * a.k : fmaf(x[e], a.k, c));
-        s += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-    }
-    return s;
-}
-
-// A batch taken into the running (m, s).  Its maximum comes first, so that the
-// sum is rescaled at most once a batch.
+// The gradient of a vector, the teacher's part left out: g / s 2^(x k - |k| m)
+// dt/dz, with the row's sum s.  Where g is positive, g / s goes into the
+// exponent c: the result is off by 2^-24 of that exponent, far below its
+// rounding to bf16.
 template <bool CAP>
-__device__ __forceinline__ void ds_take(const DsArgs& a, const uint4 (&v)[kDsBatch], int count, float& m, float& s) {
-    float mb = ds_batch_max(a, v, count);
-    if (CAP) mb = ds_arg<CAP>(a, a.sign * mb);
-    if (mb > m) {
-        s *= ds_shift<CAP>(a, m, mb);
-        m = mb;
+__device__ __forceinline__ uint4 ds_grad8(const DsArgs& a, const uint4& v, float c) {
+    float x[8];
+    ds_args8<CAP>(a, v, x);
+    const uint64_t kk = f2_packf(a.k, a.k), cc = f2_packf(c, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t x2 = f2_packf(x[2 * i], x[2 * i + 1]);
+        float lo, hi;
+        f2_unpack(f2_fma(x2, kk, cc), lo, hi);
+        uint64_t y2 = f2_packf(ds_ex2(lo), ds_ex2(hi));
+        if (CAP) {  // r (1 - r) = -x^2 - x
+            const uint64_t n2 = f2_packf(-x[2 * i], -x[2 * i + 1]);
+            y2 = f2_mul(y2, f2_fma(x2, n2, n2));
+        }
+        f2_unpack(y2, x[2 * i], x[2 * i + 1]);
     }
-    s += ds_far<CAP>(a, m) ? ds_batch_sum<CAP, true>(a, v, count, m) : ds_batch_sum<CAP, false>(a, v, count, m);
+    return round8(x);
 }
-
-// The gradient of a vector, the teacher's part left out: gs 2^(x k - |k| m)
-// dt/dz.  Where gs is positive it goes into the exponent: the result is off by
-// 2^-24 of that exponent, far below its rounding to bf16.
-template <bool CAP, bool PLAIN>
-__device__ __forceinline__ uint4 ds_grad8(const DsArgs& a, const uint4& v, float m, float c, float gs) {
+// The same for any g and m.
+template <bool CAP>
+__device__ __noinline__ uint4 ds_grad8_any(const DsArgs& a, const uint4 v, float m, float inv_s, float g) {
     float x[8];
     ds_args8<CAP>(a, v, x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float y = PLAIN ? ds_rel<CAP>(a, x[e], m) * gs : ds_ex2(fmaf(x[e], a.k, c));
-        x[e] = CAP ? y * fmaf(-x[e], x[e], -x[e]) : y;  // r (1 - r) = -x^2 - x
+        const float y = ds_rel<CAP>(a, x[e], m) * inv_s * g;
+        x[e] = CAP ? y * fmaf(-x[e], x[e], -x[e]) : y;
     }
     return round8(x);
 }
+
+// This thread's largest sign * z (-r) of a slice in global memory, and its sum
+// relative to m: for rows whose sum came out too large or too small.
+template <bool CAP, int T>
+__device__ __noinline__ float ds_slice_max(const DsArgs& a, const __nv_bfloat16* z, int n) {
+    float m = kDsLowest;
+    for (int j = threadIdx.x; j < n; j += T) m = fmaxf(m, a.sign * __bfloat162float(z[j]));
+    return CAP ? ds_arg<CAP>(a, a.sign * m) : m;
+}
+template <bool CAP, int T>
+__device__ __noinline__ float ds_slice_sum(const DsArgs& a, const __nv_bfloat16* z, int n, float m) {
+    float s = 0.0f;
+    for (int j = threadIdx.x; j < n; j += T) s += ds_rel<CAP>(a, ds_arg<CAP>(a, __bfloat162float(z[j])), m);
+    return s;
+}
+// Whether a row's sum has to be taken again: outside of this range fp32 may
+// have lost terms that count (2^-78 at least of a sum's 2^20) or the sum itself.
+__device__ __forceinline__ bool ds_lost(float s) { return !(s > 0x1p-60f && s < 0x1p100f); }
 
 // The rows' losses reduced by one block, in fp64 and a fixed order.
 __device__ __forceinline__ void ds_reduce(const DsArgs& a, double* sum) {
@@ -322,226 +398,289 @@ __device__ __forceinline__ void ds_reduce(const DsArgs& a, double* sum) {
     }
 }
 
-// Waits for part g of the row at hand.  Behind it in the queue are the row's
-// other parts and, without a gradient, those of the next row asked for since:
-// three in all.
-template <bool GRAD>
-__device__ __forceinline__ void ds_wait_part(int g) {
-    if (!GRAD || g == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    if (GRAD && g == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    if (GRAD && g == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    if (GRAD && g == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-
-template <bool GRAD, bool CAP, int T>
-__global__ void __launch_bounds__(T + 32, T == kDsMaxThreads ? 3 : 8) distill_kernel(const DsArgs a) {
+// T threads work on the slice (and kDsTeachers warps for the teacher), a chunk
+// is at most B vectors for each of them.
+template <bool GRAD, bool CAP, int T, int B>
+__global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 ? 2 : 6) distill_kernel(const DsArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ DsShared sh;
     let_next();
     constexpr int W = T / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool teaches = tid >= T;  // the last warp
-    const uint32_t rank = ds_rank(), cluster = 1u << a.log_cluster;
-    const long long stride = gridDim.x >> a.log_cluster;
+    const bool teaches = tid >= T;
+    const int rank = static_cast<int>(ds_rank()), cluster = 1 << a.log_cluster;
+    const long long first = blockIdx.x >> a.log_cluster;
+    const int stride = static_cast<int>(gridDim.x >> a.log_cluster);
+    const int rows = static_cast<int>((a.N - 1 - first) / stride + 1);  // of this cluster: not more clusters than rows
     const long long c0 = static_cast<long long>(rank) * a.slice;
     const int n = static_cast<int>(max(0LL, min(static_cast<long long>(a.slice), a.V - c0)));  // this block's logits
     const int nfull = n >> 3, ntail = n & 7;
-    const int part = (nfull + T * kDsParts - 1) / (T * kDsParts);  // a thread's vectors of a part
-    uint4* slice = reinterpret_cast<uint4*>(raw);
-    const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(slice));
+    // every chunk has `chunk` vectors but the slice's last
+    const int chunk = a.chunk, end = a.chunks - 1, rest = nfull - end * chunk;
+    uint4* ring = reinterpret_cast<uint4*>(raw);
+    float* entries = reinterpret_cast<float*>(ring + a.slots * a.chunk);
+    const int teacher_floats = (a.K + 3) / 4 * 16 + (1 << a.log_table);
+    const int cells = cluster * W;
+    uint64_t* const sums = reinterpret_cast<uint64_t*>(entries + kDsTeachers * teacher_floats);  // [kDsDepth][cells]
+    uint64_t* const sums_again = sums + kDsDepth * cells;                                       // [2][cells]
     const bool wants_loss = rank == 0 && a.loss != nullptr;
     const auto ignored = [&](long long row) { return a.labels != nullptr && row < a.N && a.labels[row] == a.ignore; };
 
-    // Part g of a row into this thread's places of the slice.
-    const auto ask = [&](int g, long long row) {
-        if (row < a.N) {
-            const __nv_bfloat16* z = a.z + row * a.ld + c0;
-            const int stop = min(nfull, (g + 1) * part * T);
-#pragma unroll 4
-            for (int j = tid + g * part * T; j < stop; j += T)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sbase + 16u * j), "l"(z + 8 * j)
-                             : "memory");
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    const auto write_zeros = [&](long long row) {
-        __nv_bfloat16* dz = a.dz + row * a.ld + c0;
-        for (int j = tid; j < nfull; j += T) __stcs(reinterpret_cast<uint4*>(dz) + j, make_uint4(0u, 0u, 0u, 0u));
-        if (tid < ntail) dz[8 * nfull + tid] = __float2bfloat16(0.0f);
-    };
-    // The first row from `row` on that takes part; those passed over are
-    // finished here (labels are the same for the whole cluster).
-    const auto taking_part = [&](long long row, bool skip) {
-        while (skip) {
-            if (GRAD && !teaches) write_zeros(row);
-            if (wants_loss && tid == T) a.loss[row] = 0.0f;
-            row += stride;
-            skip = ignored(row);
-        }
-        return row;
-    };
-
-    long long row = blockIdx.x >> a.log_cluster;
-    row = taking_part(row, ignored(row));
-    if (!teaches) {
-#pragma unroll
-        for (int g = 0; g < kDsParts; ++g) ask(g, row);
+    for (int e = tid; e < (kDsDepth + 2) * cells; e += blockDim.x) sums[e] = 0u;
+    if (tid < kDsDepth) sh.ready[tid] = sh.read[tid] = sh.told_row[tid] = 0;
+    if (tid == 0) {
+        for (int i = 0; i < kDsTeachers; ++i) mbar_init(ds_smem(&sh.done[i]), W);
+        fence_mbar_init();
+        sh.gave_up = 0;
     }
+    __syncthreads();
     ds_cluster_arrive();
-    // The teacher's warp prepares a row while the others write the gradient of
-    // the one before it.
-    DsTeacher t{}, ahead{};
-    const auto prepare = [&](DsTeacher& d, int turn, long long row) {
-        float* at = reinterpret_cast<float*>(raw + static_cast<size_t>(a.slice) * 2);
-        d.table = reinterpret_cast<int*>(at + 8 * a.K);
-        at += turn * 4 * a.K;
-        d.tp = at;
-        d.tl = at + a.K;
-        d.tx = at + 2 * a.K;
-        d.tc = reinterpret_cast<int*>(at + 3 * a.K);
-        ds_teacher<CAP>(a, d, row, c0, n, wants_loss);
-        if (lane == 0) sh.live[turn] = d.live;
-        __syncwarp();
+    const auto upstream = [&](long long row) {
+        float g = a.T * a.scale;
+        if (a.dloss != nullptr) g *= a.dloss[row * a.dloss_stride];
+        if (a.factor != nullptr) g *= a.factor[1];
+        return g;
     };
-    if (teaches && row < a.N) prepare(t, 0, row);
-    const float up = a.T * a.scale;
-    ds_cluster_wait();  // every block of the cluster runs: its shared memory may be written
-    for (int turn = 0; row < a.N; turn ^= 1) {
-        const bool skip = ignored(row + stride);
-        long long next = GRAD ? 0 : taking_part(row + stride, skip);
-        float m = CAP ? -1.0f : kDsLowest, s = 0.0f, xt = 0.0f;
-        if (!teaches) {
-            // V need not be a multiple of 8, nor the row padded: the logits
-            // behind the last whole vector go to one thread each
-            if (tid < ntail) {
-                const float zt = __bfloat162float(a.z[row * a.ld + c0 + 8 * nfull + tid]);
-                xt = ds_arg<CAP>(a, zt);
-                m = fmaxf(m, CAP ? xt : a.sign * xt);
-                s = ds_rel<CAP>(a, xt, m);
-            }
-            // the slice's maximum and sum
-#pragma unroll
-            for (int g = 0; g < kDsParts; ++g) {
-                ds_wait_part<GRAD>(g);
-                const int stop = min(nfull, (g + 1) * part * T);
-#pragma unroll 1
-                for (int j0 = tid + g * part * T; j0 < stop; j0 += kDsBatch * T) {
-                    uint4 v[kDsBatch];
-                    if (j0 + (kDsBatch - 1) * T < stop) {
-#pragma unroll
-                        for (int b = 0; b < kDsBatch; ++b) v[b] = slice[j0 + b * T];
-                        ds_take<CAP>(a, v, kDsBatch, m, s);
-                    } else {
-                        for (int j = j0; j < stop; j += T) {
-                            v[0] = slice[j];
-                            ds_take<CAP>(a, v, 1, m, s);
-                        }
-                    }
-                }
-                if (!GRAD) ask(g, next);
-            }
-            const float M = ds_warp_max(m);
-            s = ds_warp_sum(s * ds_shift<CAP>(a, m, M));
-            if (lane < static_cast<int>(cluster)) {
-                uint32_t to;
-                const uint32_t mine =
-                    static_cast<uint32_t>(__cvta_generic_to_shared(&sh.all[turn][rank * W + warp]));
-                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(lane));
-                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(M), "f"(s) : "memory");
-            }
-        }
-        __syncwarp();
-        ds_cluster_arrive();
-        ds_cluster_wait();
-        {
-            // each warp merges all warps' sums, in the same order everywhere
-            const int entries = static_cast<int>(cluster) * W;
-            const float2 none = make_float2(CAP ? -1.0f : kDsLowest, 0.0f);
-            const float2 w0 = lane < entries ? sh.all[turn][lane] : none;
-            const float2 w1 = lane + 32 < entries ? sh.all[turn][lane + 32] : none;
-            m = ds_warp_max(fmaxf(w0.x, w1.x));
-            s = ds_warp_sum(w0.y * ds_shift<CAP>(a, w0.x, m) + w1.y * ds_shift<CAP>(a, w1.x, m));
-        }
-        const bool live = sh.live[turn] != 0, far = ds_far<CAP>(a, m);
-        wait_prior();  // the factor may come from the kernel before
-        float g = up;
-        if (GRAD) {
-            next = taking_part(row + stride, skip);
-            if (a.dloss != nullptr) g *= a.dloss[row * a.dloss_stride];
-            if (a.factor != nullptr) g *= a.factor[1];
-        }
-        __nv_bfloat16* dz = GRAD ? a.dz + row * a.ld + c0 : nullptr;
-        const auto one = [&](float x, float p) {
-            const float d = (ds_rel<CAP>(a, x, m) / s - p) * g;
-            return __float2bfloat16(CAP ? 4.0f * d * fmaf(-x, x, -x) : d);
+    const auto element = [&](float z, float p, float m, float s, float g) {
+        const float d = (ds_rel<CAP>(a, z, m) / s - p) * g;
+        return __float2bfloat16(CAP ? 4.0f * d * fmaf(-z, z, -z) : d);
+    };
+    if (!teaches) {
+        // Three places in the stream: where chunks are asked for, summed, and
+        // turned into gradient; each a chunk of its row and a place in the ring.
+        const uint4* const ring_end = ring + a.slots * a.chunk;
+        uint4* ask_at = ring + tid;
+        const uint4 *sum_at = ring + tid, *out_at = ring + tid;
+        int ask_c = 0, sum_c = 0, out_c = 0, ask_i = 0, sum_i = 0, out_i = 0;
+        const long long row_step = static_cast<long long>(stride) * a.ld;
+        const uint4* ask_z = reinterpret_cast<const uint4*>(a.z + first * a.ld + c0) + tid;
+        const long long ask_step = row_step / 8 - static_cast<long long>(a.chunks) * chunk;  // from a row's end to the next
+        const __nv_bfloat16* sum_z = a.z + first * a.ld + c0;
+        uint4* out_z = nullptr;
+        long long out_row = first;
+        // whether a row is ignored: bit b of `skips` for row ask_i - b
+        uint32_t skips = ignored(first) ? 1u : 0u;
+        bool skip_next = ignored(first + stride);
+        const auto step = [&](auto& at) {
+            at += chunk;
+            if (at >= ring_end) at -= a.slots * a.chunk;
         };
-        if (!teaches) {
-            if (GRAD) {
-                if (tid < ntail) dz[8 * nfull + tid] = live ? one(xt, 0.0f) : __float2bfloat16(0.0f);
-                uint4* o = reinterpret_cast<uint4*>(dz);
-                const float gs = (CAP ? 4.0f : 1.0f) * (g / s);
-                const float c = log2f(gs) - ds_exponent<CAP>(a, m);
-#pragma unroll 1
-                for (int q = 0; q < kDsParts; ++q) {
-                    const int from = tid + q * part * T, stop = min(nfull, (q + 1) * part * T);
-                    if (live && !far && gs > 0.0f) {
-#pragma unroll 4
-                        for (int j = from; j < stop; j += T) __stcs(o + j, ds_grad8<CAP, false>(a, slice[j], m, c, gs));
-                    } else {
-                        for (int j = from; j < stop; j += T)
-                            __stcs(o + j, live ? ds_grad8<CAP, true>(a, slice[j], m, c, gs) : make_uint4(0u, 0u, 0u, 0u));
-                    }
-                    ask(q, next);
+        const auto ask = [&]() {
+            if (ask_i < rows) {
+                const int len = (skips & 1u) ? 0 : ask_c == end ? rest : chunk;
+                const uint32_t to = ds_smem(ask_at);
+#pragma unroll
+                for (int b = 0; b < B; ++b)
+                    if (tid + b * T < len)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16u * b * T), "l"(ask_z + b * T)
+                                     : "memory");
+                step(ask_at);
+                ask_z += chunk;
+                if (ask_c++ == end) {
+                    ask_c = 0;
+                    ++ask_i;
+                    ask_z += ask_step;
+                    skips = skips << 1 | (skip_next ? 1u : 0u);
+                    skip_next = ignored(first + static_cast<long long>(ask_i + 1) * stride);
                 }
-                __syncwarp();
-                asm volatile("bar.arrive 1, %0;" ::"r"(T + 32) : "memory");
             }
-        } else {
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int k = 0; k < kDsAhead; ++k) ask();
+        ds_cluster_wait();  // every block's shared memory can be stored to
+        float m = CAP ? -0.5f : 0.0f;  // the reference of sums
+        uint32_t again = 0u;           // exchanges for rows summed again
+        float sm = m, c = 0.0f;        // that of the row being summed, and - its exponent
+        uint64_t acc = 0u;
+        float om = 0.0f, os = 0.0f, og = 0.0f, oc = 0.0f;  // of the row being turned into gradient
+        bool live = false, fast = false, skip = false;
+        float up = 0.0f, dloss = a.dloss != nullptr ? a.dloss[first * a.dloss_stride] : 1.0f;  // factors of the upstream gradient
+        const int steps = rows * a.chunks;
+#pragma unroll 1
+        for (int k = 0; k < steps + a.lag; ++k) {
+            if (k < steps) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kDsAhead - 1) : "memory");
+                if (sum_c == 0) {
+                    sm = m;
+                    c = -ds_exponent(a, m);
+                    acc = 0u;
+                    skip = skips >> (ask_i - sum_i) & 1u;
+                    if (tid == 0) *static_cast<volatile float*>(&sh.reference[sum_i % kDsDepth]) = m;
+                }
+                const int len = skip ? 0 : sum_c == end ? rest : chunk;
+#pragma unroll
+                for (int b = 0; b < B; ++b)
+                    if (tid + b * T < len) {
+                        float z[8];
+                        ds_args8<CAP>(a, sum_at[b * T], z);
+                        ds_add8(a, z, c, acc);
+                    }
+                step(sum_at);
+                if (sum_c++ == end) {
+                    float lo, hi;
+                    f2_unpack(acc, lo, hi);
+                    lo += hi;
+                    // V need not be a multiple of 8, nor the row padded: the
+                    // logits behind the last whole vector go to one thread each
+                    if (!skip && tid < ntail)
+                        lo += ds_rel<CAP>(a, ds_arg<CAP>(a, __bfloat162float(sum_z[8 * nfull + tid])), sm);
+                    // (an ignored row's is 1, so that nobody sums it again)
+                    ds_send(sums + (sum_i % kDsDepth) * cells, rank * W + warp, cluster,
+                            static_cast<uint32_t>(sum_i) + 1u, skip ? 1.0f : ds_warp_sum(lo));
+                    sum_c = 0;
+                    ++sum_i;
+                    sum_z += row_step;
+                }
+            }
+            if (k >= a.lag) {
+                if (out_c == 0) {
+                    const int i = out_i;
+                    const int buf = i % kDsDepth;
+                    // The teacher's part is prepared, and block 0's teacher
+                    // reads this row's logits no more: a gradient may be
+                    // written over them.
+                    if (!ds_wait(a, sh, [&] {
+                            return ds_look(&sh.ready[buf]) >> 1 == i + 1 &&
+                                   (rank == 0 || ds_look(&sh.read[buf]) == i + 1);
+                        }))
+                        break;
+                    live = (ds_look(&sh.ready[buf]) & 1) != 0;
+                    if (!ds_receive<false>(a, sh, sums + buf * cells, cells, static_cast<uint32_t>(i) + 1u, os)) break;
+                    om = ds_look(&sh.reference[buf]);
+                    if (ds_lost(os)) {
+                        const __nv_bfloat16* z = a.z + out_row * a.ld + c0;
+                        uint64_t* cell = sums_again + (again++ & 1u) * cells;
+                        ds_send(cell, rank * W + warp, cluster, again, ds_warp_max(ds_slice_max<CAP, T>(a, z, n)));
+                        if (!ds_receive<true>(a, sh, cell, cells, again, om)) break;
+                        cell = sums_again + (again++ & 1u) * cells;
+                        ds_send(cell, rank * W + warp, cluster, again, ds_warp_sum(ds_slice_sum<CAP, T>(a, z, n, om)));
+                        if (!ds_receive<false>(a, sh, cell, cells, again, os)) break;
+                        m = om;
+                    }
+                    if (tid == 0) {
+                        *static_cast<volatile float*>(&sh.told[buf][0]) = om;
+                        *static_cast<volatile float*>(&sh.told[buf][1]) = os;
+                        __threadfence_block();
+                        *static_cast<volatile int*>(&sh.told_row[buf]) = i + 1;
+                    }
+                    if (GRAD) {
+                        if (i == 0) {
+                            wait_prior();  // the factor may come from the kernel before
+                            up = a.factor != nullptr ? a.T * a.scale * a.factor[1] : a.T * a.scale;
+                        }
+                        og = up * dloss;
+                        // asked for now, used at the next row
+                        dloss = a.dloss != nullptr && i + 1 < rows ? a.dloss[(out_row + stride) * a.dloss_stride] : 1.0f;
+                        oc = log2f(og) - log2f(os) + (CAP ? 2.0f : 0.0f) - ds_exponent(a, om);
+                        fast = live && !ds_far<CAP>(a, om) && og > 0.0f;
+                        out_z = reinterpret_cast<uint4*>(a.dz + out_row * a.ld + c0) + tid;
+                    }
+                }
+                if (GRAD) {
+                    const int len = out_c == end ? rest : chunk;
+                    if (fast) {
+#pragma unroll
+                        for (int b = 0; b < B; ++b)
+                            if (tid + b * T < len) __stcs(out_z + b * T, ds_grad8<CAP>(a, out_at[b * T], oc));
+                    } else {
+#pragma unroll 1
+                        for (int b = 0; tid + b * T < len; ++b)
+                            __stcs(out_z + b * T, live ? ds_grad8_any<CAP>(a, out_at[b * T], om, 1.0f / os, CAP ? 4.0f * og : og)
+                                                       : make_uint4(0u, 0u, 0u, 0u));
+                    }
+                    out_z += chunk;
+                    step(out_at);
+                }
+                if (out_c++ == end) {
+                    if (GRAD) {
+                        if (tid < ntail) {
+                            const long long at = out_row * a.ld + c0 + 8 * nfull + tid;
+                            a.dz[at] = live ? element(ds_arg<CAP>(a, __bfloat162float(a.z[at])), 0.0f, om, os, og)
+                                            : __float2bfloat16(0.0f);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(ds_smem(&sh.done[out_i % kDsTeachers]));
+                    }
+                    out_c = 0;
+                    ++out_i;
+                    out_row += stride;
+                }
+            }
+            ask();
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else {
+        DsTeacher t{};
+        t.tp = entries + (warp - W) * teacher_floats;
+        t.tl = t.tp + a.K;
+        t.tx = t.tl + a.K;
+        t.tc = reinterpret_cast<int*>(t.tx + a.K);
+        t.table = reinterpret_cast<int*>(t.tp + (a.K + 3) / 4 * 16);
+        ds_cluster_wait();
+        for (int i = warp - W; i < rows; i += kDsTeachers) {
+            const long long row = first + static_cast<long long>(i) * stride;
+            const int buf = i % kDsDepth;
+            t.live = t.bad = false;
+            if (!ignored(row)) ds_teacher<CAP>(a, t, row, c0, n, wants_loss);
+            __threadfence_block();  // what was read of the logits has arrived: it is in tx
+            __syncwarp();
+            if (lane == 0) *static_cast<volatile int*>(&sh.ready[buf]) = (i + 1) * 2 + t.live;
+            if (rank == 0 && lane < cluster)
+                asm volatile("st.volatile.shared::cluster.u32 [%0], %1;" ::"r"(
+                                 ds_remote(ds_smem(&sh.read[buf]), static_cast<uint32_t>(lane))),
+                             "r"(i + 1)
+                             : "memory");
+            __syncwarp();
+            if (!ds_wait(a, sh, [&] { return ds_look(&sh.told_row[buf]) == i + 1; })) break;
+            __threadfence_block();
+            const float m = ds_look(&sh.told[buf][0]), s = ds_look(&sh.told[buf][1]);
+            wait_prior();
             if (wants_loss) {
+                const bool far = ds_far<CAP>(a, m);
                 const float log_s = logf(s);
                 constexpr float kLn2 = 0.6931471805599453f;
                 float sum = 0.0f;
-                for (int i = lane; i < a.K; i += 32) {
-                    const float p = t.tp[i] * t.inv_psum;
-                    if (p == 0.0f || t.tc[i] < 0) continue;
-                    const float x = far ? (t.tx[i] - a.sign * m) * a.k
-                                        : fmaf(t.tx[i], a.k, -ds_exponent<CAP>(a, m));
-                    sum += p * ((t.tl[i] - t.log_psum) - (x * kLn2 - log_s));
+                for (int e = lane; t.live && e < a.K; e += 32) {
+                    const float p = t.tp[e] * t.inv_psum;
+                    if (p == 0.0f || t.tc[e] < 0) continue;
+                    const float y = far ? (t.tx[e] - a.sign * m) * a.k : fmaf(t.tx[e], a.k, -ds_exponent(a, m));
+                    sum += p * ((t.tl[e] - t.log_psum) - (y * kLn2 - log_s));
                 }
                 sum = ds_warp_sum(sum);
-                if (lane == 0)
-                    a.loss[row] = t.bad ? __int_as_float(0x7fc00000) : (live ? a.T * a.T * sum : 0.0f);
+                if (lane == 0) a.loss[row] = t.bad ? __int_as_float(0x7fc00000) : (t.live ? a.T * a.T * sum : 0.0f);
             }
-            if (t.bad && rank == 0 && lane == 0) atomicExch(a.status, -1);
-            if (next < a.N) prepare(ahead, turn ^ 1, next);
+            if (t.bad && rank == 0 && lane == 0) atomicExch(a.status, kStatusBad);
             if (GRAD) {
-                asm volatile("bar.sync 1, %0;" ::"r"(T + 32) : "memory");  // the row's gradient is written
-                for (int i = lane; live && i < a.K; i += 32) {
-                    const int c = t.tc[i];
-                    const long long at = c - c0;
-                    if (c < 0 || at < 0 || at >= n) continue;
-                    float p = t.tp[i];
+                const float g = upstream(row);
+                const uint32_t done = ds_smem(&sh.done[warp - W]), parity = static_cast<uint32_t>(i / kDsTeachers) & 1u;
+                if (!ds_wait(a, sh, [&] { return mbar_try_wait(done, parity); })) break;
+                __nv_bfloat16* dz = a.dz + row * a.ld;
+                for (int e = lane; t.live && e < a.K; e += 32) {
+                    const int c = t.tc[e];
+                    if (c < c0 || c >= c0 + n) continue;
+                    float p = t.tp[e];
                     if (t.twice) {  // the first entry of an id writes for all of them
-                        bool first = true;
+                        bool before = false;
                         p = 0.0f;
                         for (int o = 0; o < a.K; ++o) {
                             if (t.tc[o] != c) continue;
-                            first = first && o >= i;
+                            before = before || o < e;
                             p += t.tp[o];
                         }
-                        if (!first) continue;
+                        if (before) continue;
                     }
-                    dz[at] = one(t.tx[i], p * t.inv_psum);
+                    dz[c] = element(t.tx[e], p * t.inv_psum, m, s, g);
                 }
                 __syncwarp();
             }
-            t = ahead;
         }
-        row = next;
     }
-    wait_prior();  // in every block, whatever rows it had
-    if (a.out == nullptr || rank != 0) return;
-    __syncthreads();  // this block's losses are written
+    wait_prior();  // in every thread, whatever it did
+    __syncthreads();
+    ds_cluster_arrive();
+    ds_cluster_wait();  // no block leaves while another may still store to it
+    if (a.out == nullptr || rank != 0 || sh.gave_up) return;
     if (tid == 0) {
         __threadfence();
         sh.last = atomicAdd(a.counter, 1u) == static_cast<uint32_t>(stride - 1);

@@ -19,8 +19,6 @@
 namespace lmlp {
 namespace step {
 
-constexpr int kStatusBad = -1;  // LORA_MLP_ERR_INVALID_ARG
-
 // ----------------------------------------------------------------------------- lookup
 
 constexpr int kEmbThreads = 256;

@@ -583,8 +583,9 @@ int lora_qk_rope_backward(const lora_qk_shape* shape, const lora_qk_view* q, con
 
 namespace {
 
-constexpr int64_t kDsMaxV = int64_t{kDsMaxCluster} * 94208;  // 184 KB of shared memory a block
-constexpr size_t kDsMaxSmem = 2 * 94208 + kDsMaxK * (kDsEntryBytes + 2 * 4);
+constexpr size_t kDsMaxSmem = 226 * 1024;  // a block's, beside its static part
+constexpr int kDsMaxCluster = 8;
+constexpr int64_t kDsMaxV = 5 << 16;  // what eight blocks hold with kDsMaxK teacher's entries
 
 int validate_distill(const lora_distill_shape* sh) {
     if (sh == nullptr) return LORA_MLP_ERR_INVALID_ARG;
@@ -626,36 +627,78 @@ DsArgs ds_args(const lora_distill_shape* sh, const void* logits, const void* val
     a.k = static_cast<float>(kn * kLog2e);
     if (sh->softcap > 0.0f) a.cap2 = static_cast<float>(2.0 * a.scale / sh->softcap * kLog2e);
     a.status = status;
+    a.wait_limit = 4000000000LL;  // about 2 s
     return a;
 }
 
-// Slices of 64 KB at most (three or four blocks a multiprocessor, so that
-// loads, arithmetic and stores of different rows overlap), larger ones only
-// where eight blocks have no room for the row otherwise; more blocks a row
-// where there are too few rows for the multiprocessors.
-int launch_distill(const char* name, DsArgs a, int sms, cudaStream_t st, bool after_own) {
-    a.log_cluster = 0;
-    const auto slice = [&a](int log_cluster) { return (((a.V + (1 << log_cluster) - 1) >> log_cluster) + 7) / 8 * 8; };
-    while (a.log_cluster < 3 &&
-           (slice(a.log_cluster) > 32768 || ((a.N << a.log_cluster) * 2 <= sms && slice(a.log_cluster) > 4096)))
-        ++a.log_cluster;
-    a.slice = static_cast<int>(slice(a.log_cluster));
-    const bool wide = a.slice > 4096;  // below, a thread of a block of 256 would have fewer than two vectors
-    const int threads = (wide ? kDsMaxThreads : kDsMinThreads) + 32;
-    const size_t smem = std::max(static_cast<size_t>(a.slice) * 2 + static_cast<size_t>(a.K) * kDsEntryBytes +
-                                     (size_t{4} << a.log_table),
-                                 static_cast<size_t>(threads) * 12);  // 12: the reduction's sums and counts
+// A launch that is settled but for its call, so that a refusal comes before the
+// first kernel of an entry.
+struct DsLaunch {
+    DsArgs a;
+    void (*kernel)(DsArgs);
+    int threads, cluster;
+    int64_t clusters;
+    size_t smem;
+};
+
+// T threads for a slice, chunks of at most B vectors each.  The smallest
+// cluster whose blocks hold their slice and the chunks around it in shared
+// memory; a larger one where there are too few rows for the multiprocessors.
+template <int T, int B>
+int plan_distill_by(const DsArgs& args, int sms, DsLaunch& l) {
+    constexpr int64_t widest = T * B;  // vectors of a chunk
+    l.a = args;
+    DsArgs& a = l.a;
+    l.threads = T + 32 * kDsTeachers;
     const bool grad = a.dz != nullptr, cap = a.cap > 0.0f;
-    auto kernel = wide ? (grad ? (cap ? distill_kernel<true, true, kDsMaxThreads> : distill_kernel<true, false, kDsMaxThreads>)
-                               : (cap ? distill_kernel<false, true, kDsMaxThreads> : distill_kernel<false, false, kDsMaxThreads>))
-                       : (grad ? (cap ? distill_kernel<true, true, kDsMinThreads> : distill_kernel<true, false, kDsMinThreads>)
-                               : (cap ? distill_kernel<false, true, kDsMinThreads> : distill_kernel<false, false, kDsMinThreads>));
+    const auto fixed = [&](int lc) {
+        return kDsTeachers * ((static_cast<size_t>(a.K) + 3) / 4 * 4 * kDsEntryBytes + (size_t{4} << a.log_table)) +
+               static_cast<size_t>(kDsDepth + 2) * (T / 32 * 8 << lc);
+    };
+    const auto slice = [&](int lc) { return (((a.V + (1 << lc) - 1) >> lc) + 7) / 8; };
+    const auto chunks = [&](int lc) { return (slice(lc) + widest - 1) / widest; };
+    const auto chunk = [&](int lc) { return (slice(lc) + chunks(lc) - 1) / chunks(lc); };
+    const auto most = [&](int lc) { return static_cast<int64_t>((kDsMaxSmem - fixed(lc)) / (chunk(lc) * 16)); };
+    int lc = 0;
+    while ((1 << lc) < kDsMaxCluster && ((grad && chunks(lc) + 1 + kDsAhead > most(lc)) ||
+                                         ((a.N << lc) * 2 <= sms && chunks(lc) > 1)))
+        ++lc;
+    a.log_cluster = lc;
+    a.slice = static_cast<int>(slice(lc) * 8);
+    a.chunks = static_cast<int>(chunks(lc));
+    a.chunk = static_cast<int>(chunk(lc));
+    // a chunk more than the row's, where there is room: the sums' way to the
+    // other blocks is then hidden behind it
+    a.lag = a.chunks + (a.chunks > 1 && (!grad || a.chunks + 2 + kDsAhead <= most(lc)) ? 2 : 1);
+    a.slots = (grad ? a.lag : 0) + kDsAhead;
+    if (a.slots > most(lc)) return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
+    l.cluster = 1 << lc;
+    l.smem = std::max(static_cast<size_t>(a.slots) * a.chunk * 16 + fixed(lc),
+                      static_cast<size_t>(l.threads) * 12);  // 12: the reduction's sums and counts
+    l.kernel = grad ? (cap ? distill_kernel<true, true, T, B> : distill_kernel<true, false, T, B>)
+                    : (cap ? distill_kernel<false, true, T, B> : distill_kernel<false, false, T, B>);
     // As many clusters as run at once; each takes every so many-th row.
     int at_once = 0;
-    STEP_TRY(resident_clusters(kernel, kDsMaxSmem, threads, smem, 1 << a.log_cluster, &at_once));
-    const int64_t clusters = std::min<int64_t>(a.N, at_once);
-    return launch(name, kernel, dim3(static_cast<unsigned>(clusters << a.log_cluster)),
-                  dim3(static_cast<unsigned>(threads)), smem, st, after_own, 1 << a.log_cluster, a);
+    STEP_TRY(resident_clusters(l.kernel, kDsMaxSmem, l.threads, l.smem, l.cluster, &at_once));
+    l.clusters = std::min<int64_t>(a.N, at_once);
+    return LORA_MLP_OK;
+}
+
+// The gradient takes an SM for each block: 512 threads and chunks of 24 KB (453
+// us at 4096 rows of 128256; 460 with 16 KB), which do not fit where a row is
+// long and K large.  The loss alone needs no row resident: blocks of 256
+// threads, two an SM, 24 KB a chunk (107 us there; 111 with 16 KB).  Short rows
+// take blocks of 64 threads, so that a thread has work to overlap.
+int plan_distill(const DsArgs& a, int sms, DsLaunch& l) {
+    if (a.V <= 4096) return plan_distill_by<64, 4>(a, sms, l);
+    if (a.dz == nullptr) return plan_distill_by<256, 6>(a, sms, l);
+    const int rc = plan_distill_by<512, 3>(a, sms, l);
+    return rc == LORA_MLP_ERR_UNSUPPORTED_SHAPE ? plan_distill_by<512, 2>(a, sms, l) : rc;
+}
+
+int launch_distill(const char* name, const DsLaunch& l, cudaStream_t st, bool after_own) {
+    return launch(name, l.kernel, dim3(static_cast<unsigned>(l.clusters * l.cluster)), dim3(l.threads), l.smem, st,
+                  after_own, l.cluster, l.a);
 }
 
 int check_distill(const lora_distill_shape* sh, const void* logits, const void* values, const void* ids,
@@ -680,7 +723,9 @@ int lora_distill_forward(const lora_distill_shape* shape, const void* logits, co
     STEP_TRY(device_info(&di));
     DsArgs a = ds_args(shape, logits, values, ids, labels, di.status);
     a.loss = loss;
-    return launch_distill("DISTILL_fwd", a, di.sms, static_cast<cudaStream_t>(stream), false);
+    DsLaunch l;
+    STEP_TRY(plan_distill(a, di.sms, l));
+    return launch_distill("DISTILL_fwd", l, static_cast<cudaStream_t>(stream), false);
 }
 
 int lora_distill_backward(const lora_distill_shape* shape, const void* logits, const void* values, const void* ids,
@@ -695,7 +740,9 @@ int lora_distill_backward(const lora_distill_shape* shape, const void* logits, c
     a.dloss = dloss;
     a.dloss_stride = 1;
     a.dz = static_cast<__nv_bfloat16*>(dlogits);
-    return launch_distill("DISTILL_bwd", a, di.sms, static_cast<cudaStream_t>(stream), false);
+    DsLaunch l;
+    STEP_TRY(plan_distill(a, di.sms, l));
+    return launch_distill("DISTILL_bwd", l, static_cast<cudaStream_t>(stream), false);
 }
 
 int lora_distill_backward_reduced(const lora_distill_shape* shape, const void* logits, const void* values,
@@ -711,7 +758,9 @@ int lora_distill_backward_reduced(const lora_distill_shape* shape, const void* l
     a.dloss = dout;
     a.factor = fwd_out;
     a.dz = static_cast<__nv_bfloat16*>(dlogits);
-    return launch_distill("DISTILL_bwd", a, di.sms, static_cast<cudaStream_t>(stream), false);
+    DsLaunch l;
+    STEP_TRY(plan_distill(a, di.sms, l));
+    return launch_distill("DISTILL_bwd", l, static_cast<cudaStream_t>(stream), false);
 }
 
 int lora_distill_sizes(const lora_distill_shape* shape, size_t* workspace_bytes) {
@@ -744,9 +793,11 @@ int lora_distill_loss(const lora_distill_shape* shape, const void* logits, const
     a.out = out;
     a.factor = out;
     a.mean = mean;
+    DsLaunch l;
+    STEP_TRY(plan_distill(a, di.sms, l));
     STEP_TRY(launch("DISTILL_count", distill_count_kernel, dim3(1), kDsCountThreads, 0, st, false, 1, a.labels, a.N,
                     a.ignore, a.mean, out, a.counter));
-    return launch_distill(dlogits != nullptr ? "DISTILL_loss_grad" : "DISTILL_fwd", a, di.sms, st, true);
+    return launch_distill(dlogits != nullptr ? "DISTILL_loss_grad" : "DISTILL_fwd", l, st, true);
 }
 
 }  // extern "C"

@@ -6,6 +6,8 @@
 namespace lmlp {
 namespace step {
 
+constexpr int kStatusBad = -1;  // LORA_MLP_ERR_INVALID_ARG
+
 __device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

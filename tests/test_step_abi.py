@@ -166,7 +166,7 @@ def ds_shape(N=4, V=100, ld=104, K=8, T=1.0, s=1.0, cap=0.0, vt=1, it=1):
     (dict(it=-1), _lib.ERR_INVALID_ARG),
     (dict(ld=100), _lib.ERR_UNSUPPORTED_SHAPE),
     (dict(K=1025), _lib.ERR_UNSUPPORTED_SHAPE),
-    (dict(V=753665, ld=753672), _lib.ERR_UNSUPPORTED_SHAPE),
+    (dict(V=327681, ld=327688), _lib.ERR_UNSUPPORTED_SHAPE),
 ])
 def test_distill_shape_validation(L, kw, code):
     ws = ctypes.c_size_t()
