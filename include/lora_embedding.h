@@ -41,8 +41,8 @@ int lora_embedding_forward(int64_t N, int64_t V, int64_t d, float scale, const i
  * of ids that many tokens share).  Host only. */
 int lora_embedding_sizes(int64_t N, int64_t V, int64_t d, size_t* workspace_bytes);
 
-/* dE [V, d] from dOut [N, d] and ids [N].  padding_idx < 0: none.  Two
- * launches for N <= 8192; above, two more and one for each 9 bits of V. */
+/* dE [V, d] from dOut [N, d] and ids [N].  padding_idx < 0: none.  Three
+ * launches for N <= 8192; above, three and one for each 9 bits of V. */
 int lora_embedding_backward(int64_t N, int64_t V, int64_t d, float scale, int64_t padding_idx, int grad_type,
                             const int64_t* ids, const void* dOut, void* dE, void* workspace,
                             size_t workspace_bytes, void* stream);

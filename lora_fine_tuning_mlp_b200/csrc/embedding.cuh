@@ -24,7 +24,9 @@ namespace step {
 constexpr int kEmbThreads = 256;
 
 // A row is walked by `tpr` threads (a power of two, at most the block), 16
-// bytes at a time; a block holds kEmbThreads / tpr rows.
+// bytes at a time, up to kEmbLoads of them in flight a thread; a block holds
+// kEmbThreads / tpr rows.
+constexpr int kEmbLoads = 4;
 struct EmbFwdArgs {
     const long long* ids;
     const __nv_bfloat16* E;
@@ -50,7 +52,7 @@ __global__ void __launch_bounds__(kEmbThreads) embed_fwd_kernel(const EmbFwdArgs
         return;
     }
     const uint4* e = reinterpret_cast<const uint4*>(a.E) + id * a.nv;
-    constexpr int U = 4;
+    constexpr int U = kEmbLoads;
     for (int j0 = lane; j0 < a.nv; j0 += U * step) {
         uint4 v[U];
 #pragma unroll
@@ -63,7 +65,7 @@ __global__ void __launch_bounds__(kEmbThreads) embed_fwd_kernel(const EmbFwdArgs
             widen8(v[u], f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] *= a.scale;
-            o[j0 + u * step] = round8(f);
+            __stcs(o + j0 + u * step, round8(f));
         }
     }
 }
@@ -78,10 +80,7 @@ constexpr int kSortMaxBits = 9;
 constexpr int kSortMaxBins = 1 << kSortMaxBits;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortSmallItems = 8;                                  // one block sorts up to 8192 tokens
-constexpr int kSortSmall = kSortThreads * kSortSmallItems;
-constexpr int kSortTileItems = 4;                                   // a tile of the many-block sort
-constexpr int kSortTile = kSortThreads * kSortTileItems;
+constexpr int kSortSmall = kSortThreads * 8;  // tokens that one block sorts
 
 struct SortArgs {
     const long long* ids;
@@ -91,6 +90,7 @@ struct SortArgs {
     int bits;           // digit width
     int passes;
     int ntiles;
+    int tile;           // tokens of a tile: kSortThreads, once or four times
     uint32_t *key[2], *val[2];  // [N] each; the result is in key[passes & 1], val[passes & 1]
     uint32_t* hist;             // [passes][ntiles][bins]
     uint32_t* counters;         // zeroed here for the gradient kernel
@@ -111,6 +111,7 @@ struct SortShared {
     uint16_t warp_bin[kSortWarps][kSortMaxBins];  // counts, then each warp's start within its bin
     uint32_t bin_total[kSortMaxBins];
     uint32_t bin_start[kSortMaxBins];
+    uint32_t bin_before[kSortMaxBins];
     uint32_t scan[kSortWarps];
 };
 
@@ -179,46 +180,47 @@ __device__ __forceinline__ void bin_starts(SortShared& s, const uint32_t* total,
 // Up to kSortSmall tokens: one block, every pass in shared memory.  The
 // gradient kernel may start at once: what it does before it waits for this
 // one (zeroing rows) needs nothing from here.
+template <int IPT>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_small_kernel(const SortArgs a) {
     let_next();
     extern __shared__ __align__(16) unsigned char raw[];
     SortShared& s = *reinterpret_cast<SortShared*>(raw);
     uint32_t* skey = reinterpret_cast<uint32_t*>(raw + sizeof(SortShared));
-    uint32_t* sval = skey + kSortSmall;
+    uint32_t* sval = skey + kSortThreads * IPT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < a.ncounters; i += kSortThreads) a.counters[i] = 0u;
-    uint32_t key[kSortSmallItems], val[kSortSmallItems];
+    uint32_t key[IPT], val[IPT];
 #pragma unroll
-    for (int k = 0; k < kSortSmallItems; ++k) {
-        const int i = warp * 32 * kSortSmallItems + 32 * k + lane;
+    for (int k = 0; k < IPT; ++k) {
+        const int i = warp * 32 * IPT + 32 * k + lane;
         key[k] = i < a.N ? sort_key(a, a.ids[i]) : 0xFFFFFFFFu;  // past the end: sorts last
         val[k] = static_cast<uint32_t>(i);
     }
     const int bins = 1 << a.bits;
     for (int p = 0; p < a.passes; ++p) {
-        uint32_t digit[kSortSmallItems], rank[kSortSmallItems];
+        uint32_t digit[IPT], rank[IPT];
 #pragma unroll
-        for (int k = 0; k < kSortSmallItems; ++k) digit[k] = (key[k] >> (p * a.bits)) & (bins - 1);
+        for (int k = 0; k < IPT; ++k) digit[k] = (key[k] >> (p * a.bits)) & (bins - 1);
         block_ranks(s, digit, bins, rank);
         bin_starts(s, s.bin_total, s.bin_start, bins);
 #pragma unroll
-        for (int k = 0; k < kSortSmallItems; ++k) {
+        for (int k = 0; k < IPT; ++k) {
             const uint32_t at = s.bin_start[digit[k]] + rank[k];
             skey[at] = key[k];
             sval[at] = val[k];
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kSortSmallItems; ++k) {
-            const int i = warp * 32 * kSortSmallItems + 32 * k + lane;
+        for (int k = 0; k < IPT; ++k) {
+            const int i = warp * 32 * IPT + 32 * k + lane;
             key[k] = skey[i];
             val[k] = sval[i];
         }
         __syncthreads();
     }
 #pragma unroll
-    for (int k = 0; k < kSortSmallItems; ++k) {
-        const int i = warp * 32 * kSortSmallItems + 32 * k + lane;
+    for (int k = 0; k < IPT; ++k) {
+        const int i = warp * 32 * IPT + 32 * k + lane;
         if (i < a.N) {
             (a.passes & 1 ? a.key[1] : a.key[0])[i] = key[k];
             (a.passes & 1 ? a.val[1] : a.val[0])[i] = val[k];
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_small_kernel(const So
     }
 }
 
-// More tokens: tiles of kSortTile.  First the digit counts of every tile for
+// More tokens: tiles, one to a block.  First the digit counts of every tile for
 // pass 0 (and zeros for the other passes), then one scatter a pass; a scatter
 // counts the next pass's digits by the tile each key lands in (whole numbers:
 // their order does not matter).
@@ -240,8 +242,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_count_kernel(const So
     }
     for (int i = tile * kSortThreads + threadIdx.x; i < a.ncounters; i += gridDim.x * kSortThreads) a.counters[i] = 0u;
     __syncthreads();
-    for (int k = 0; k < kSortTileItems; ++k) {
-        const long long i = static_cast<long long>(tile) * kSortTile + k * kSortThreads + threadIdx.x;
+    for (int k = threadIdx.x; k < a.tile; k += kSortThreads) {
+        const long long i = static_cast<long long>(tile) * a.tile + k;
         if (i < a.N) {
             const uint32_t key = sort_key(a, a.ids[i]);
             atomicAdd(&cnt[key & (bins - 1)], 1u);
@@ -252,6 +254,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_count_kernel(const So
 }
 
 // Pass p: reads the ids (p = 0) or key/val[p & 1], writes key/val[(p + 1) & 1].
+template <int IPT>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_scatter_kernel(const SortArgs a, int p) {
     extern __shared__ __align__(16) unsigned char raw[];
     SortShared& s = *reinterpret_cast<SortShared*>(raw);
@@ -262,10 +265,10 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_scatter_kernel(const 
     const bool last = p == a.passes - 1;
     const uint32_t *skey = p & 1 ? a.key[1] : a.key[0], *sval = p & 1 ? a.val[1] : a.val[0];
     uint32_t *dkey = p & 1 ? a.key[0] : a.key[1], *dval = p & 1 ? a.val[0] : a.val[1];
-    uint32_t key[kSortTileItems], val[kSortTileItems], digit[kSortTileItems], rank[kSortTileItems];
+    uint32_t key[IPT], val[IPT], digit[IPT], rank[IPT];
 #pragma unroll
-    for (int k = 0; k < kSortTileItems; ++k) {
-        const long long i = static_cast<long long>(tile) * kSortTile + warp * 32 * kSortTileItems + 32 * k + lane;
+    for (int k = 0; k < IPT; ++k) {
+        const long long i = static_cast<long long>(tile) * (kSortThreads * IPT) + warp * 32 * IPT + 32 * k + lane;
         const bool in = i < a.N;
         if (p == 0) {
             key[k] = in ? sort_key(a, a.ids[i]) : 0xFFFFFFFFu;
@@ -276,32 +279,36 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_scatter_kernel(const 
         }
         digit[k] = (key[k] >> (p * a.bits)) & (bins - 1);
     }
-    // this tile's start in each bin, and the bins' totals
+    // this tile's start in each bin, and the bins' totals; the halves of the
+    // block take every other tile
+    const int bin = threadIdx.x & (kSortMaxBins - 1), half = threadIdx.x / kSortMaxBins;
     uint32_t before = 0u, total = 0u;
-    if (static_cast<int>(threadIdx.x) < bins) {
-        const uint32_t* h = a.hist + static_cast<size_t>(p) * a.ntiles * bins + threadIdx.x;
-#pragma unroll 8
-        for (int t = 0; t < a.ntiles; ++t) {
+    if (bin < bins) {
+        const uint32_t* h = a.hist + static_cast<size_t>(p) * a.ntiles * bins + bin;
+#pragma unroll 16
+        for (int t = half; t < a.ntiles; t += 2) {
             const uint32_t c = h[static_cast<size_t>(t) * bins];
             if (t < tile) before += c;
             total += c;
         }
-        s.bin_total[threadIdx.x] = total;
+        if (half == 1) s.bin_total[bin] = total, s.bin_before[bin] = before;
     }
     __syncthreads();
+    if (half == 0 && bin < bins) s.bin_total[bin] += total;
+    __syncthreads();
     bin_starts(s, s.bin_total, s.bin_start, bins);
-    if (static_cast<int>(threadIdx.x) < bins) s.bin_start[threadIdx.x] += before;
+    if (half == 0 && bin < bins) s.bin_start[bin] += before + s.bin_before[bin];
     __syncthreads();
     block_ranks(s, digit, bins, rank);
 #pragma unroll
-    for (int k = 0; k < kSortTileItems; ++k) {
-        const long long i = static_cast<long long>(tile) * kSortTile + warp * 32 * kSortTileItems + 32 * k + lane;
+    for (int k = 0; k < IPT; ++k) {
+        const long long i = static_cast<long long>(tile) * (kSortThreads * IPT) + warp * 32 * IPT + 32 * k + lane;
         if (i >= a.N) continue;
         const uint32_t at = s.bin_start[digit[k]] + rank[k];
         dkey[at] = key[k];
         dval[at] = val[k];
         if (!last)
-            atomicAdd(a.hist + (static_cast<size_t>(p + 1) * a.ntiles + at / kSortTile) * bins +
+            atomicAdd(a.hist + (static_cast<size_t>(p + 1) * a.ntiles + at / (kSortThreads * IPT)) * bins +
                           ((key[k] >> ((p + 1) * a.bits)) & (bins - 1)),
                       1u);
     }
@@ -309,25 +316,38 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_scatter_kernel(const 
 
 // ----------------------------------------------------------------------------- the gradient
 
-// A "worker" is kEmbThreads threads or, where a row has fewer 16-byte vectors,
-// as many warps as it has 32s of them; it writes `rows_w` consecutive rows of
-// dE.  It finds its rows' tokens by a search of the sorted ids, writes zeros
-// up to the next id that occurs, and sums that id's tokens in registers.
+// Zeros for all of dE, while the tokens are sorted: many small blocks, which
+// the hardware starts in the order of their addresses, write 7.4 TB/s; blocks
+// that stay and take several parts, wherever these lie, 6.3.
+constexpr int kZeroThreads = 256;
+constexpr int kZeroStores = 4;  // of 16 bytes, a thread
+constexpr int kZeroBlock = kZeroThreads * kZeroStores;
+
+__global__ void __launch_bounds__(kZeroThreads) embed_zero_kernel(uint4* out, long long n) {
+    let_next();
+    const long long i = static_cast<long long>(blockIdx.x) * kZeroBlock + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kZeroStores; ++k)
+        if (i + k * kZeroThreads < n) out[i + k * kZeroThreads] = make_uint4(0u, 0u, 0u, 0u);
+    // nothing here needs the sort, but who waits for this kernel relies on it
+    if (blockIdx.x == gridDim.x - 1) wait_prior();
+}
+
+// A "worker" is the power of two of threads, 32 .. kEmbThreads, that has two
+// vectors of a row each, at most (or as often as the row asks for it).  Worker
+// p looks at place p of the sorted tokens.  Where an id begins, it sums that
+// id's tokens in registers and writes the row.
 //
 // An id that takes many tokens (padding, a space) would keep one worker busy
 // long after the others: the sorted tokens are therefore also cut into chunks
-// of kEmbChunk, and a chunk that lies wholly within one id is summed by a
-// block of its own into `part`.  Whoever is last of an id's chunk blocks and
-// its row's worker (a counter for each slice of columns) adds up the tokens
-// before the first whole chunk, the chunks' sums and the tokens behind the
-// last one, in that order: the same sum whoever is last.
-//
-// The first `first_wave` row blocks write zeros over all their rows before
-// they wait for the sort, which keeps the memory busy while one block sorts;
-// the few rows with tokens are written a second time.
-constexpr int kEmbChunk = 64;
-constexpr int kEmbBlockBytes = 65536;  // of dE a row block writes
-constexpr int kEmbBlocksPerSm = 4;     // row blocks of the first wave
+// of kEmbChunk, and a chunk that lies wholly within one id is summed into
+// `part`, a block for each slice of the row: groups of its threads, two vectors
+// a thread, take a share of the tokens each and the shares are added up in
+// order.  Whichever of an id's chunks is last (a counter for each slice) adds up
+// the tokens before the first whole chunk, the chunks' sums and the tokens
+// behind the last one, shared out in the same way: the same sum whichever is
+// last.
+constexpr int kEmbChunk = 32;
 
 struct EmbBwdArgs {
     const uint32_t* key;  // sorted ids [N], V for tokens that take no part
@@ -337,10 +357,9 @@ struct EmbBwdArgs {
     float* part;         // [N / kEmbChunk][8 nv]
     uint32_t* counters;  // [N / kEmbChunk][slices], zero
     int N, V, nv;
-    int slices;      // of kEmbThreads vectors
-    int log_worker;  // threads of a worker: 32 .. kEmbThreads
-    int rows_w;
-    int first_wave;
+    int slices;
+    int log_group;   // threads of a group: half a slice's vectors
+    int log_worker;
     float scale;
 };
 
@@ -358,84 +377,89 @@ __device__ __forceinline__ int lower_bound(const uint32_t* key, int lo, int hi, 
     return lo + __popc(__ballot_sync(0xffffffffu, lo + lane < hi && key[lo + lane] < x));
 }
 
-// acc += the rows of tokens val[from, to), vector j of each.
-__device__ __forceinline__ void add_tokens(const EmbBwdArgs& a, int from, int to, int j, float (&acc)[8]) {
+// acc[h] += the rows of tokens val[from, to), vector j + h * step of each.
+__device__ __forceinline__ void add_tokens(const EmbBwdArgs& a, int from, int to, int j, int step,
+                                           float (&acc)[2][8]) {
     constexpr int U = 4;
     const uint4* d = reinterpret_cast<const uint4*>(a.dOut) + j;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const bool first = j < a.nv, second = j + step < a.nv;
 #pragma unroll 1
     for (int p = from; p < to; p += U) {
-        uint4 v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            v[u] = p + u < to ? load_once(d + static_cast<long long>(a.val[p + u]) * a.nv) : make_uint4(0u, 0u, 0u, 0u);
+        uint4 v[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float f[8];
-            widen8(v[u], f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += f[i];
+            const uint4* row = d + static_cast<long long>(p + u < to ? a.val[p + u] : 0u) * a.nv;
+            v[u][0] = p + u < to && first ? load_once(row) : zero;
+            v[u][1] = p + u < to && second ? load_once(row + step) : zero;
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float f[8];
+                widen8(v[u][h], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[h][i] += f[i];
+            }
     }
 }
 
 template <bool F32>
-__device__ __forceinline__ void store_grad(const EmbBwdArgs& a, long long row, int j, float (&acc)[8]) {
+__device__ __forceinline__ void store_grad(const EmbBwdArgs& a, uint32_t row, int j, int step, float (&acc)[2][8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] *= a.scale;
-    const long long at = row * a.nv + j;
-    if (F32) {
-        float4* o = reinterpret_cast<float4*>(a.dE) + 2 * at;
-        o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-    } else {
-        reinterpret_cast<uint4*>(a.dE)[at] = round8(acc);
-    }
-}
-
-// Slice `sl` of the row of an id with tokens [s, e) and whole chunks [c0, c1).
-template <bool F32>
-__device__ __noinline__ void finish_slice(const EmbBwdArgs& a, uint32_t row, int s, int e, int c0, int c1, int sl,
-                                             int tid, int threads) {
-    const int end = min(a.nv, (sl + 1) * kEmbThreads);
-    for (int j = sl * kEmbThreads + tid; j < end; j += threads) {
-        float acc[8] = {};
-        add_tokens(a, s, c0 * kEmbChunk, j, acc);
-        const float4* p = reinterpret_cast<const float4*>(a.part) + 2 * (static_cast<long long>(c0) * a.nv + j);
-        constexpr int U = 4;
-#pragma unroll 1
-        for (int c = c0; c < c1; c += U) {
-            float4 v[U][2];
+    for (int h = 0; h < 2; ++h) {
+        if (j + h * step >= a.nv) continue;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float4* q = p + 2 * static_cast<long long>(c - c0 + u) * a.nv;
-                v[u][0] = c + u < c1 ? __ldcg(q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                v[u][1] = c + u < c1 ? __ldcg(q + 1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                acc[0] += v[u][0].x, acc[1] += v[u][0].y, acc[2] += v[u][0].z, acc[3] += v[u][0].w;
-                acc[4] += v[u][1].x, acc[5] += v[u][1].y, acc[6] += v[u][1].z, acc[7] += v[u][1].w;
-            }
+        for (int i = 0; i < 8; ++i) acc[h][i] *= a.scale;
+        const long long at = static_cast<long long>(row) * a.nv + j + h * step;
+        if (F32) {
+            float4* o = reinterpret_cast<float4*>(a.dE) + 2 * at;
+            o[0] = make_float4(acc[h][0], acc[h][1], acc[h][2], acc[h][3]);
+            o[1] = make_float4(acc[h][4], acc[h][5], acc[h][6], acc[h][7]);
+        } else {
+            reinterpret_cast<uint4*>(a.dE)[at] = round8(acc[h]);
         }
-        add_tokens(a, c1 * kEmbChunk, e, j, acc);
-        store_grad<F32>(a, row, j, acc);
     }
 }
 
-// One chunk and slice of columns: its sum, and the row if it comes last.
+// The groups' shares, added up in order by the first.
+__device__ __forceinline__ void join_shares(int group, float (&acc)[2][8]) {
+    __shared__ float shares[2][8][kEmbThreads];
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) shares[h][i][threadIdx.x] = acc[h][i];
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) >= group) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            for (int t = threadIdx.x + group; t < kEmbThreads; t += group) acc[h][i] += shares[h][i][t];
+}
+
+// One chunk and slice: its sum, and the row's if it comes last.
 template <bool F32>
 __device__ void chunk_block(const EmbBwdArgs& a, int chunk, int sl) {
     const int from = chunk * kEmbChunk;
     const uint32_t id = a.key[from];
     if (id >= static_cast<uint32_t>(a.V) || a.key[from + kEmbChunk - 1] != id) return;
-    const int j = sl * kEmbThreads + threadIdx.x;
-    if (j < a.nv) {
-        float acc[8] = {};
-        add_tokens(a, from, from + kEmbChunk, j, acc);
-        float4* p = reinterpret_cast<float4*>(a.part) + 2 * (static_cast<long long>(chunk) * a.nv + j);
-        __stcg(p, make_float4(acc[0], acc[1], acc[2], acc[3]));
-        __stcg(p + 1, make_float4(acc[4], acc[5], acc[6], acc[7]));
-    }
+    const int group = 1 << a.log_group, groups = kEmbThreads >> a.log_group, share = kEmbChunk / groups;
+    const int g = threadIdx.x >> a.log_group;
+    const int j = sl * 2 * group + (threadIdx.x & (group - 1));
+    float acc[2][8] = {};
+    add_tokens(a, from + g * share, from + (g + 1) * share, j, group, acc);
+    join_shares(group, acc);
+    if (g == 0)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (j + h * group < a.nv) {
+                float4* p = reinterpret_cast<float4*>(a.part) + 2 * (static_cast<long long>(chunk) * a.nv + j + h * group);
+                __stcg(p, make_float4(acc[h][0], acc[h][1], acc[h][2], acc[h][3]));
+                __stcg(p + 1, make_float4(acc[h][4], acc[h][5], acc[h][6], acc[h][7]));
+            }
     const int s = lower_bound(a.key, 0, from, id), e = lower_bound(a.key, from, a.N, id + 1u);
     const int c0 = (s + kEmbChunk - 1) / kEmbChunk, c1 = e / kEmbChunk;
     __shared__ uint32_t arrived;
@@ -443,71 +467,77 @@ __device__ void chunk_block(const EmbBwdArgs& a, int chunk, int sl) {
     __syncthreads();
     if (threadIdx.x == 0) arrived = atomicAdd(a.counters + static_cast<long long>(c0) * a.slices + sl, 1u);
     __syncthreads();
-    if (arrived != static_cast<uint32_t>(c1 - c0)) return;  // c1 - c0 chunks and the row's worker
+    if (arrived != static_cast<uint32_t>(c1 - c0 - 1)) return;
     __threadfence();
-    finish_slice<F32>(a, id, s, e, c0, c1, sl, threadIdx.x, kEmbThreads);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[h][i] = 0.0f;
+    const int before = c0 * kEmbChunk, behind = c1 * kEmbChunk;
+    add_tokens(a, min(s + g * share, before), min(s + (g + 1) * share, before), j, group, acc);
+    const int each = (c1 - c0 + groups - 1) / groups;
+    const int first = min(c0 + g * each, c1), last = min(first + each, c1);
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    constexpr int U = 2;
+#pragma unroll 1
+    for (int c = first; c < last; c += U) {
+        float4 v[U][2][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool in = c + u < last && j + h * group < a.nv;
+                const float4* q =
+                    reinterpret_cast<const float4*>(a.part) + 2 * (static_cast<long long>(c + u) * a.nv + j + h * group);
+                v[u][h][0] = in ? __ldcg(q) : zero;
+                v[u][h][1] = in ? __ldcg(q + 1) : zero;
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    acc[h][4 * k] += v[u][h][k].x, acc[h][4 * k + 1] += v[u][h][k].y;
+                    acc[h][4 * k + 2] += v[u][h][k].z, acc[h][4 * k + 3] += v[u][h][k].w;
+                }
+    }
+    add_tokens(a, min(behind + g * share, e), min(behind + (g + 1) * share, e), j, group, acc);
+    join_shares(group, acc);
+    if (g == 0) store_grad<F32>(a, id, j, group, acc);
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kEmbThreads, kEmbBlocksPerSm) embed_bwd_kernel(const EmbBwdArgs a) {
-    // block order: the first wave of row blocks, the chunks, the other row blocks
-    const int nchunk_blocks = a.N / kEmbChunk * a.slices;
-    int rb = blockIdx.x;
-    if (rb >= a.first_wave) {
-        rb -= a.first_wave;
-        if (rb < nchunk_blocks) {
-            wait_prior();
-            chunk_block<F32>(a, rb / a.slices, rb % a.slices);
-            return;
-        }
-        rb += a.first_wave - nchunk_blocks;
-    }
-    const int threads = 1 << a.log_worker, workers = kEmbThreads >> a.log_worker;
-    const int tid = threadIdx.x & (threads - 1), w = threadIdx.x >> a.log_worker;
-    const long long first = (static_cast<long long>(rb) * workers + w) * a.rows_w;
-    const long long r0 = min(first, static_cast<long long>(a.V)), r1 = min(first + a.rows_w, static_cast<long long>(a.V));
-    constexpr int kOut = F32 ? 2 : 1;  // 16-byte stores of a vector
-    uint4* out = static_cast<uint4*>(a.dE);
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const bool early = rb < a.first_wave;
-    if (early)
-        for (long long i = r0 * a.nv * kOut + tid; i < r1 * a.nv * kOut; i += threads) out[i] = zero;
+__global__ void __launch_bounds__(kEmbThreads, 4) embed_bwd_kernel(const EmbBwdArgs a) {
     wait_prior();
-    if (early) __threadfence();  // before this worker counts itself in at a row that others may write
-    __syncthreads();
-    if (r0 >= r1) return;
-    int p = lower_bound(a.key, 0, a.N, static_cast<uint32_t>(r0));
-    const int hi = lower_bound(a.key, p, a.N, static_cast<uint32_t>(r1));
-    long long r = r0;
-    while (r < r1) {
-        const long long next = p < hi ? static_cast<long long>(a.key[p]) : r1;
-        if (!early)
-            for (long long i = r * a.nv * kOut + tid; i < next * a.nv * kOut; i += threads) out[i] = zero;
-        if (next >= r1) break;
-        const uint32_t id = static_cast<uint32_t>(next);
-        const int s = p, e = lower_bound(a.key, p, hi, id + 1u);
-        const int c0 = (s + kEmbChunk - 1) / kEmbChunk, c1 = e / kEmbChunk;
-        if (c0 < c1) {
-            // the chunks' blocks write this row, or this worker does if it comes last
-            for (int sl = 0; sl < a.slices; ++sl) {
-                __shared__ uint32_t seen[kEmbThreads / 32];  // the worker's threads learn one count
-                asm volatile("bar.sync %0, %1;" ::"r"(w + 1), "r"(threads) : "memory");
-                if (tid == 0) seen[w] = atomicAdd(a.counters + static_cast<long long>(c0) * a.slices + sl, 1u);
-                asm volatile("bar.sync %0, %1;" ::"r"(w + 1), "r"(threads) : "memory");
-                if (seen[w] == static_cast<uint32_t>(c1 - c0)) {
-                    __threadfence();
-                    finish_slice<F32>(a, id, s, e, c0, c1, sl, tid, threads);
-                }
-            }
-        } else {
-            for (int j = tid; j < a.nv; j += threads) {
-                float acc[8] = {};
-                add_tokens(a, s, e, j, acc);
-                store_grad<F32>(a, next, j, acc);
-            }
+    const int chunk_blocks = a.N / kEmbChunk * a.slices;
+    if (static_cast<int>(blockIdx.x) < chunk_blocks) {
+        chunk_block<F32>(a, blockIdx.x / a.slices, blockIdx.x % a.slices);
+        return;
+    }
+    const int threads = 1 << a.log_worker, lane = threadIdx.x & 31;
+    const long long p = (static_cast<long long>(blockIdx.x - chunk_blocks) << (8 - a.log_worker)) +
+                        (threadIdx.x >> a.log_worker);
+    static_assert(kEmbThreads == 1 << 8, "the workers of a block");
+    if (p >= a.N) return;
+    const int s = static_cast<int>(p);
+    const uint32_t id = a.key[s];
+    if (id >= static_cast<uint32_t>(a.V) || (s > 0 && a.key[s - 1] == id)) return;
+    // the id's end, as far as it can lie without a whole chunk
+    int n = 0;
+    for (; n < 2 * kEmbChunk; n += 32) {
+        const unsigned same = __ballot_sync(0xffffffffu, s + n + lane < a.N && a.key[min(s + n + lane, a.N - 1)] == id);
+        if (same != 0xffffffffu) {
+            n += __ffs(~same) - 1;
+            break;
         }
-        p = e;
-        r = next + 1;
+    }
+    const int e = s + n;
+    if ((s + kEmbChunk - 1) / kEmbChunk < e / kEmbChunk) return;  // its chunks' blocks write the row
+    for (int j = threadIdx.x & (threads - 1); j < a.nv; j += 2 * threads) {
+        float acc[2][8] = {};
+        add_tokens(a, s, e, j, threads, acc);
+        store_grad<F32>(a, id, j, threads, acc);
     }
 }
 

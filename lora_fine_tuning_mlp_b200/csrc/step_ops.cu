@@ -289,7 +289,7 @@ int validate_embedding(int64_t N, int64_t V, int64_t d) {
 }
 
 struct EmbPlan {
-    int nv, slices, nchunks, bits, passes, ntiles;
+    int nv, slices, log_worker, log_group, nchunks, bits, passes, ntiles, tile;
     bool small;
     size_t key[2], val[2], hist, counters, part, total;
 };
@@ -297,13 +297,21 @@ struct EmbPlan {
 EmbPlan make_emb_plan(int64_t N, int64_t V, int64_t d) {
     EmbPlan p{};
     p.nv = static_cast<int>(d / 8);
-    p.slices = (p.nv + kEmbThreads - 1) / kEmbThreads;
+    p.log_worker = std::max(5, ceil_log2(static_cast<uint64_t>(std::min((p.nv + 1) / 2, kEmbThreads))));
     p.nchunks = static_cast<int>(N / kEmbChunk);
+    // Narrow slices, for many groups a block and few tokens a share, unless
+    // there are so many chunks that most of their blocks find nothing to do.
+    p.log_group = 5;
+    while (p.log_group < p.log_worker && int64_t{p.nchunks} * (p.nv >> (p.log_group + 1)) > 1024) ++p.log_group;
+    p.slices = (p.nv + (2 << p.log_group) - 1) >> (p.log_group + 1);
     const int key_bits = std::max(1, ceil_log2(static_cast<uint64_t>(V) + 1));  // keys 0 .. V
     p.passes = (key_bits + kSortMaxBits - 1) / kSortMaxBits;
     p.bits = (key_bits + p.passes - 1) / p.passes;
     p.small = N <= kSortSmall;
-    p.ntiles = static_cast<int>((N + kSortTile - 1) / kSortTile);
+    // a tile a multiprocessor as far as that goes; four times as wide beyond,
+    // as every tile reads every tile's counts
+    p.tile = kSortThreads * (N <= int64_t{128} * kSortThreads ? 1 : 4);
+    p.ntiles = static_cast<int>((N + p.tile - 1) / p.tile);
     Carver c;
     for (int i = 0; i < 2; ++i) {
         p.key[i] = c.take(static_cast<size_t>(N) * 4);
@@ -335,7 +343,11 @@ int lora_embedding_forward(int64_t N, int64_t V, int64_t d, float scale, const i
     a.N = N;
     a.V = V;
     a.nv = static_cast<int>(d / 8);
-    a.log_tpr = ceil_log2(static_cast<uint64_t>(std::min(a.nv, kEmbThreads)));
+    // Few tokens: a thread for each vector of a row.  Many: kEmbLoads vectors a
+    // thread, so that enough bytes are on their way.
+    const bool many = N * a.nv >= int64_t{kEmbLoads} * kEmbThreads * 8 * di.sms;
+    const int per = many ? kEmbLoads : 1;
+    a.log_tpr = ceil_log2(static_cast<uint64_t>(std::min((a.nv + per - 1) / per, kEmbThreads)));
     a.scale = scale;
     a.status = di.status;
     const int rows = kEmbThreads >> a.log_tpr;
@@ -357,6 +369,11 @@ int lora_embedding_backward(int64_t N, int64_t V, int64_t d, float scale, int64_
     if (grad_type != LORA_EMBEDDING_GRAD_BF16 && grad_type != LORA_EMBEDDING_GRAD_FP32) return LORA_MLP_ERR_INVALID_ARG;
     STEP_TRY(check_args({{ids, 8}, {dOut, 16}, {dE, 16}, {workspace, 16}}));
     const EmbPlan p = make_emb_plan(N, V, d);
+    const bool f32 = grad_type == LORA_EMBEDDING_GRAD_FP32;
+    const int64_t zeros = V * d / 8 * (f32 ? 2 : 1), zero_blocks = (zeros + kZeroBlock - 1) / kZeroBlock;
+    const int64_t workers = kEmbThreads >> p.log_worker;
+    const int64_t blocks = (N + workers - 1) / workers + static_cast<int64_t>(p.nchunks) * p.slices;
+    if (zero_blocks > INT32_MAX || blocks > INT32_MAX) return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
     if (workspace_bytes < p.total) return LORA_MLP_ERR_WORKSPACE_TOO_SMALL;
     STEP_TRY(check_memory({{ids, 8}, {dOut, 16}, {dE, 16}, {workspace, 16}}));
     DevInfo di;
@@ -372,6 +389,7 @@ int lora_embedding_backward(int64_t N, int64_t V, int64_t d, float scale, int64_
     s.bits = p.bits;
     s.passes = p.passes;
     s.ntiles = p.ntiles;
+    s.tile = p.tile;
     for (int i = 0; i < 2; ++i) {
         s.key[i] = reinterpret_cast<uint32_t*>(ws + p.key[i]);
         s.val[i] = reinterpret_cast<uint32_t*>(ws + p.val[i]);
@@ -381,15 +399,21 @@ int lora_embedding_backward(int64_t N, int64_t V, int64_t d, float scale, int64_
     s.ncounters = p.nchunks * p.slices;
     s.status = di.status;
     if (p.small) {
-        const size_t smem = sizeof(SortShared) + 2 * sizeof(uint32_t) * kSortSmall;
-        STEP_TRY(allow_smem(embed_sort_small_kernel, smem));
-        STEP_TRY(launch("EMB_sort", embed_sort_small_kernel, dim3(1), kSortThreads, smem, st, false, 1, s));
+        const int items = N <= kSortThreads ? 1 : N <= 2 * kSortThreads ? 2 : N <= 4 * kSortThreads ? 4 : 8;
+        auto kernel = items == 1   ? embed_sort_small_kernel<1>
+                      : items == 2 ? embed_sort_small_kernel<2>
+                      : items == 4 ? embed_sort_small_kernel<4>
+                                   : embed_sort_small_kernel<8>;
+        const size_t smem = sizeof(SortShared) + 2 * sizeof(uint32_t) * kSortThreads * items;
+        STEP_TRY(allow_smem(kernel, smem));
+        STEP_TRY(launch("EMB_sort", kernel, dim3(1), kSortThreads, smem, st, false, 1, s));
     } else {
         const dim3 grid(static_cast<unsigned>(p.ntiles));
         STEP_TRY(launch("EMB_sort_count", embed_sort_count_kernel, grid, kSortThreads, 0, st, false, 1, s));
         for (int i = 0; i < p.passes; ++i)
-            STEP_TRY(launch("EMB_sort_scatter", embed_sort_scatter_kernel, grid, kSortThreads, sizeof(SortShared), st,
-                            true, 1, s, i));
+            STEP_TRY(launch("EMB_sort_scatter",
+                            p.tile == kSortThreads ? embed_sort_scatter_kernel<1> : embed_sort_scatter_kernel<4>, grid,
+                            kSortThreads, sizeof(SortShared), st, true, 1, s, i));
     }
 
     EmbBwdArgs a{};
@@ -403,19 +427,12 @@ int lora_embedding_backward(int64_t N, int64_t V, int64_t d, float scale, int64_
     a.V = s.V;
     a.nv = p.nv;
     a.slices = p.slices;
-    a.log_worker = std::max(5, ceil_log2(static_cast<uint64_t>(std::min(p.nv, kEmbThreads))));
+    a.log_group = p.log_group;
+    a.log_worker = p.log_worker;
     a.scale = scale;
-    // Rows of a worker: about kEmbBlockBytes of dE a block, but eight blocks a
-    // multiprocessor where the vocabulary is small.
-    const bool f32 = grad_type == LORA_EMBEDDING_GRAD_FP32;
-    const int64_t workers = kEmbThreads >> a.log_worker, row_bytes = d * (f32 ? 4 : 2);
-    const int64_t by_bytes = kEmbBlockBytes / (row_bytes * workers), spread = int64_t{8} * di.sms * workers;
-    a.rows_w = static_cast<int>(std::max<int64_t>(1, std::min(by_bytes, (V + spread - 1) / spread)));
-    const int64_t nrow = (V + a.rows_w * workers - 1) / (a.rows_w * workers);
-    const int64_t blocks = nrow + static_cast<int64_t>(p.nchunks) * p.slices;
-    if (blocks > INT32_MAX) return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
-    a.first_wave = static_cast<int>(std::min<int64_t>(nrow, int64_t{kEmbBlocksPerSm} * di.sms));
     const dim3 grid(static_cast<unsigned>(blocks));
+    STEP_TRY(launch("EMB_zero", embed_zero_kernel, dim3(static_cast<unsigned>(zero_blocks)),
+                    kZeroThreads, 0, st, true, 1, static_cast<uint4*>(dE), static_cast<long long>(zeros)));
     if (f32) return launch("EMB_grad", embed_bwd_kernel<true>, grid, kEmbThreads, 0, st, true, 1, a);
     return launch("EMB_grad", embed_bwd_kernel<false>, grid, kEmbThreads, 0, st, true, 1, a);
 }
