@@ -31,7 +31,8 @@
  * 16-byte aligned; their gradients fp32 [D], 4-byte aligned.  positions are
  * int64, 8-byte aligned: entry b * position_stride + s, in [0, P); NULL means
  * position s.  B, S, Hq, Hk >= 1; D and rot multiples of 16,
- * 16 <= rot <= D <= 512.  Other conventions: lora_step.h.
+ * 16 <= rot <= D <= 512; B S (ceil(Hq / 2) + ceil(Hk / 2)) below 2^31.  Other
+ * conventions: lora_step.h.
  *
  * A position outside [0, P) is a device-side finding: the heads of its token
  * get NaN (and add nothing to dgain), and lora_step_device_status reports

@@ -433,11 +433,11 @@ __device__ __forceinline__ void join_shares(int group, float (&acc)[2][8]) {
         for (int i = 0; i < 8; ++i) shares[h][i][threadIdx.x] = acc[h][i];
     __syncthreads();
     if (static_cast<int>(threadIdx.x) >= group) return;
+    for (int t = threadIdx.x + group; t < kEmbThreads; t += group)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            for (int t = threadIdx.x + group; t < kEmbThreads; t += group) acc[h][i] += shares[h][i][t];
+            for (int i = 0; i < 8; ++i) acc[h][i] += shares[h][i][t];
 }
 
 // One chunk and slice: its sum, and the row's if it comes last.

@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "f32x2.cuh"
 #include "vec8.cuh"
 
 namespace lmlp {
@@ -24,11 +25,22 @@ namespace step {
 
 constexpr int kQkThreads = 128;
 constexpr int kQkWarps = kQkThreads / 32;
-constexpr int kQkUnroll = 4;
+// heads of a thread in the forward; without the norm fewer, in blocks of 64 registers a thread
+constexpr int kQkUnroll = 4, kQkRopeUnroll = 2;
+constexpr int kQkBwdBlocksPerSm = 3;  // of the backward through the norm, by its registers
 
 struct QkView {
     uint4* p;
     long long sb, ss, sh;  // in 16-byte vectors
+};
+
+// Quotients of numbers below 2^31 by a divisor that is known at the launch, by
+// a multiplication (Granlund and Montgomery, 1994): with 2^(l - 1) < d <= 2^l
+// and m = floor(2^32 (2^l - d) / d) + 1, n / d = (mulhi(m, n) + n) >> l.
+struct QkDivisor {
+    uint32_t d, m;
+    int l;
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (__umulhi(m, n) + n) >> l; }
 };
 
 struct QkArgs {
@@ -38,7 +50,9 @@ struct QkArgs {
     const float *cos, *sin;
     const long long* pos;
     long long pos_stride;
-    long long T, S, P;
+    long long T, P;
+    QkDivisor seq;                              // S
+    QkDivisor per_token, per_query, per_key;    // a token's units
     int H[2];
     int D, nslot, nrot, half;  // nslot = D/16 threads of a head do work, nrot = rot/16 of them turn pairs
     int log_group;
@@ -62,201 +76,292 @@ __device__ __forceinline__ void qk_vectors(const QkArgs& a, int slot, int& v0, i
     }
 }
 
-// The 8 angles of `slot` at position p.
-__device__ __forceinline__ void qk_angles(const QkArgs& a, long long p, int slot, float (&c)[8], float (&s)[8]) {
-    if (slot < a.nrot) {
-        const float4* cp = reinterpret_cast<const float4*>(a.cos + p * a.half) + 2 * slot;
-        const float4* sp = reinterpret_cast<const float4*>(a.sin + p * a.half) + 2 * slot;
-        const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
-        c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-        s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+// The values of two vectors as the two sides of the pairs that a thread turns,
+// two pairs to a packed fp32 pair: sides of pair 2i and 2i + 1 in x[i] and y[i].
+struct QkPairs {
+    uint64_t x[4], y[4];
+};
+
+__device__ __forceinline__ uint32_t qk_low(uint32_t w) { return w << 16; }
+__device__ __forceinline__ uint32_t qk_high(uint32_t w) { return w & 0xFFFF0000u; }
+
+template <bool INTER>
+__device__ __forceinline__ QkPairs qk_widen(const uint4& v0, const uint4& v1) {
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    QkPairs r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] *= a.turn;
+    for (int i = 0; i < 4; ++i) {
+        if (INTER) {
+            r.x[i] = f2_pack(qk_low(w[2 * i]), qk_low(w[2 * i + 1]));
+            r.y[i] = f2_pack(qk_high(w[2 * i]), qk_high(w[2 * i + 1]));
+        } else {
+            r.x[i] = f2_pack(qk_low(w[i]), qk_high(w[i]));
+            r.y[i] = f2_pack(qk_low(w[4 + i]), qk_high(w[4 + i]));
+        }
     }
+    return r;
+}
+
+__device__ __forceinline__ uint32_t qk_bf16x2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 template <bool INTER>
-__device__ __forceinline__ void qk_rotate(float (&f)[2][8], const float (&c)[8], const float (&s)[8]) {
+__device__ __forceinline__ void qk_round(const QkPairs& r, uint4& v0, uint4& v1) {
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float& x = INTER ? f[i >> 2][2 * (i & 3)] : f[0][i];
-        float& y = INTER ? f[i >> 2][2 * (i & 3) + 1] : f[1][i];
-        const float a = x, b = y;
-        x = a * c[i] - b * s[i];
-        y = b * c[i] + a * s[i];
+    for (int i = 0; i < 4; ++i) {
+        float x0, x1, y0, y1;
+        f2_unpack(r.x[i], x0, x1);
+        f2_unpack(r.y[i], y0, y1);
+        w[INTER ? 2 * i : i] = INTER ? qk_bf16x2(x0, y0) : qk_bf16x2(x0, x1);
+        w[INTER ? 2 * i + 1 : 4 + i] = INTER ? qk_bf16x2(x1, y1) : qk_bf16x2(y0, y1);
+    }
+    v0 = make_uint4(w[0], w[1], w[2], w[3]);
+    v1 = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// The 8 angles of `slot` at position p: cosines in x and sines in y.
+struct QkAngles {
+    uint64_t c[4], s[4];
+};
+__device__ __forceinline__ QkAngles qk_angles(const QkArgs& a, long long p, int slot) {
+    const float4* cp = reinterpret_cast<const float4*>(a.cos + p * a.half) + 2 * slot;
+    const float4* sp = reinterpret_cast<const float4*>(a.sin + p * a.half) + 2 * slot;
+    const uint64_t turn = f2_packf(a.turn, a.turn);
+    QkAngles r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 c = __ldg(cp + i), s = __ldg(sp + i);
+        r.c[2 * i] = f2_packf(c.x, c.y), r.c[2 * i + 1] = f2_packf(c.z, c.w);
+        r.s[2 * i] = f2_mul(f2_packf(s.x, s.y), turn), r.s[2 * i + 1] = f2_mul(f2_packf(s.z, s.w), turn);
+    }
+    return r;
+}
+
+__device__ __forceinline__ void qk_rotate(QkPairs& f, const QkAngles& a) {
+    const uint64_t minus = f2_packf(-1.0f, -1.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t x = f.x[i], y = f.y[i];
+        f.x[i] = f2_fma(x, a.c[i], f2_mul(f2_mul(y, minus), a.s[i]));
+        f.y[i] = f2_fma(y, a.c[i], f2_mul(x, a.s[i]));
     }
 }
 
-// Sum over the lanes of a group, the same for each of them.
-__device__ __forceinline__ float group_sum(float v, int group) {
-    for (int o = group >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+__device__ __forceinline__ float qk_lanes(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return lo + hi;
+}
+// sum of p q over a thread's values
+__device__ __forceinline__ float qk_dot(const QkPairs& p, const QkPairs& q) {
+    uint64_t v = f2_mul(p.x[0], q.x[0]);
+    uint64_t w = f2_mul(p.y[0], q.y[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        v = f2_fma(p.x[i], q.x[i], v);
+        w = f2_fma(p.y[i], q.y[i], w);
+    }
+    return qk_lanes(f2_add(v, w));
+}
+
+// Sums over the lanes of a group, the same for each of them.
+template <int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], int group) {
+    for (int o = group >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
 __device__ __forceinline__ uint4 qk_nan() { return make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u); }
 
-// A warp's unit: one token and kQkUnroll * (32 / group) heads of its queries
+// A warp's unit: one token and U * (32 / group) heads of its queries
 // or of its keys.
 template <bool NORM, bool INTER>
-__global__ void __launch_bounds__(kQkThreads) qk_rope_kernel(const QkArgs a) {
-    const long long unit = static_cast<long long>(blockIdx.x) * kQkWarps + (threadIdx.x >> 5);
-    const int per_token = a.units[0] + a.units[1];
-    const long long t = unit / per_token;
+__global__ void __launch_bounds__(kQkThreads, NORM ? 4 : 8) qk_rope_kernel(const QkArgs a) {
+    constexpr int U = NORM ? kQkUnroll : kQkRopeUnroll;
+    const uint32_t unit = blockIdx.x * kQkWarps + (threadIdx.x >> 5);
+    const uint32_t t = a.per_token.quotient(unit);
     if (t >= a.T) return;
-    int chunk = static_cast<int>(unit - t * per_token);
+    int chunk = static_cast<int>(unit - t * a.per_token.d);
     const int kind = chunk >= a.units[0];
     if (kind) chunk -= a.units[0];
     const int lane = threadIdx.x & 31, group = 1 << a.log_group, slot = lane & (group - 1);
-    const long long b = t / a.S, s = t - b * a.S;
+    const uint32_t b = a.seq.quotient(t), s = t - b * a.seq.d;
     const QkView in = kind ? a.in[1] : a.in[0], out = kind ? a.out[1] : a.out[0];
     const int H = kind ? a.H[1] : a.H[0];
     const int rows = 32 >> a.log_group;
-    const int h0 = chunk * rows * kQkUnroll + (lane >> a.log_group);
+    const int h0 = chunk * rows * U + (lane >> a.log_group);
     const bool works = slot < a.nslot;
     int v0, v1;
     qk_vectors<INTER>(a, slot, v0, v1);
-    const uint4* ip = in.p + b * in.sb + s * in.ss;
-    uint4 v[kQkUnroll][2];
+    const uint4* ip = in.p + b * in.sb + s * in.ss + h0 * in.sh;
+    const long long next = rows * in.sh;
+    uint4 v[U][2];
 #pragma unroll
-    for (int u = 0; u < kQkUnroll; ++u) {
-        const int h = h0 + u * rows;
+    for (int u = 0; u < U; ++u) {
         v[u][0] = v[u][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (works && h < H) {
-            v[u][0] = load_once(ip + h * in.sh + v0);
-            v[u][1] = load_once(ip + h * in.sh + v1);
+        if (works && h0 + u * rows < H) {
+            v[u][0] = load_once(ip + v0);
+            v[u][1] = load_once(ip + v1);
         }
+        ip += next;
     }
-    float g[2][8];
+    QkPairs g{};
     if (NORM && works) {
         const uint4* gp = kind ? a.gain[1] : a.gain[0];
-        widen8(__ldg(gp + v0), g[0]);
-        widen8(__ldg(gp + v1), g[1]);
+        g = qk_widen<INTER>(__ldg(gp + v0), __ldg(gp + v1));
     }
     const long long p = a.pos != nullptr ? a.pos[b * a.pos_stride + s] : s;
     const bool bad = p < 0 || p >= a.P;
-    if (bad && lane == 0) atomicExch(a.status, -1);
-    float c[8], sn[8];
-    if (works && !bad) qk_angles(a, p, slot, c, sn);
-    uint4* op = out.p + b * out.sb + s * out.ss;
+    if (bad && lane == 0) atomicExch(a.status, kStatusBad);
+    const bool turns = slot < a.nrot && !bad;
+    QkAngles ang{};
+    if (turns) ang = qk_angles(a, p, slot);
+    float ss[U];
+    if (NORM) {
 #pragma unroll
-    for (int u = 0; u < kQkUnroll; ++u) {
-        const int h = h0 + u * rows;
-        float f[2][8];
-        widen8(v[u][0], f[0]);
-        widen8(v[u][1], f[1]);
+        for (int u = 0; u < U; ++u) {
+            const QkPairs f = qk_widen<INTER>(v[u][0], v[u][1]);
+            ss[u] = qk_dot(f, f);
+        }
+        group_sums(ss, group);
+    }
+    uint4* op = out.p + b * out.sb + s * out.ss + h0 * out.sh;
+    const long long out_next = rows * out.sh;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        QkPairs f = qk_widen<INTER>(v[u][0], v[u][1]);
         if (NORM) {
-            float ss = 0.0f;
+            const float r = rsqrtf(ss[u] * a.inv_d + a.eps);
+            const uint64_t rr = f2_packf(r, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(f[0][i], f[0][i], fmaf(f[1][i], f[1][i], ss));
-            const float r = 1.0f / sqrtf(group_sum(ss, group) * a.inv_d + a.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f[0][i] *= r * g[0][i];
-                f[1][i] *= r * g[1][i];
+            for (int i = 0; i < 4; ++i) {
+                f.x[i] = f2_mul(f2_mul(f.x[i], rr), g.x[i]);
+                f.y[i] = f2_mul(f2_mul(f.y[i], rr), g.y[i]);
             }
         }
-        if (!works || h >= H) continue;
-        if (slot < a.nrot) qk_rotate<INTER>(f, c, sn);
-        op[h * out.sh + v0] = bad ? qk_nan() : round8(f[0]);
-        op[h * out.sh + v1] = bad ? qk_nan() : round8(f[1]);
+        if (turns) qk_rotate(f, ang);
+        if (works && h0 + u * rows < H) {
+            uint4 o0, o1;
+            qk_round<INTER>(f, o0, o1);
+            op[v0] = bad ? qk_nan() : o0;
+            op[v1] = bad ? qk_nan() : o1;
+        }
+        op += out_next;
     }
 }
 
-// Backward through the norm.  A warp takes every gridDim-th unit of its kind,
-// so that it can add up dn xh over all of them in registers; a block's sums go
-// to `part`, which qk_gain_kernel adds up in block order.
+// Backward through the norm.  With e = dn gain (dn = R(p)^T dy) and r the
+// reciprocal root, dx = r e - x r^3 mean(e x): both sums of a head are taken
+// over x itself and joined in one go.  A warp takes every gridDim-th unit of
+// its kind, so that it can add up dn x r over all of them in registers; a
+// block's sums go to `part`, which qk_gain_kernel adds up in block order.
 constexpr int kQkBwdUnroll = 2;
 
 template <bool INTER>
-__global__ void __launch_bounds__(kQkThreads) qk_rope_bwd_kernel(const QkArgs a) {
+__global__ void __launch_bounds__(kQkThreads, kQkBwdBlocksPerSm) qk_rope_bwd_kernel(const QkArgs a) {
     __shared__ float sums[kQkWarps][512];
     const int kind = static_cast<int>(blockIdx.x) >= a.blocks_q;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = 1 << a.log_group, slot = lane & (group - 1), rows = 32 >> a.log_group;
-    const long long nblocks = kind ? gridDim.x - a.blocks_q : a.blocks_q;
-    const long long first = (kind ? blockIdx.x - a.blocks_q : blockIdx.x) * static_cast<long long>(kQkWarps) + warp;
+    const uint32_t nblocks = kind ? gridDim.x - a.blocks_q : a.blocks_q;
+    const uint32_t first = (kind ? blockIdx.x - a.blocks_q : blockIdx.x) * kQkWarps + warp;
     const QkView dy = kind ? a.in[1] : a.in[0], dx = kind ? a.out[1] : a.out[0], x = kind ? a.x[1] : a.x[0];
-    const int H = kind ? a.H[1] : a.H[0], per_token = kind ? a.units[1] : a.units[0];
+    const int H = kind ? a.H[1] : a.H[0];
+    const QkDivisor per_token = kind ? a.per_key : a.per_query;
     const bool works = slot < a.nslot;
     int v0, v1;
     qk_vectors<INTER>(a, slot, v0, v1);
-    float g[2][8] = {}, acc[2][8] = {};
+    QkPairs g{}, acc{};
     if (works) {
         const uint4* gp = kind ? a.gain[1] : a.gain[0];
-        widen8(__ldg(gp + v0), g[0]);
-        widen8(__ldg(gp + v1), g[1]);
+        g = qk_widen<INTER>(__ldg(gp + v0), __ldg(gp + v1));
     }
     let_next();
-    for (long long unit = first; unit < a.T * per_token; unit += nblocks * kQkWarps) {
-        const long long t = unit / per_token;
-        const int chunk = static_cast<int>(unit - t * per_token);
-        const long long b = t / a.S, s = t - b * a.S;
-        const int h0 = chunk * rows * kQkBwdUnroll + (lane >> a.log_group);
-        const uint4 *yp = dy.p + b * dy.sb + s * dy.ss, *xp = x.p + b * x.sb + s * x.ss;
+    const uint32_t units = static_cast<uint32_t>(a.T) * per_token.d;
+    for (uint32_t unit = first; unit < units; unit += nblocks * kQkWarps) {
+        const uint32_t t = per_token.quotient(unit), chunk = unit - t * per_token.d;
+        const uint32_t b = a.seq.quotient(t), s = t - b * a.seq.d;
+        const int h0 = static_cast<int>(chunk) * rows * kQkBwdUnroll + (lane >> a.log_group);
+        const uint4* yp = dy.p + b * dy.sb + s * dy.ss + h0 * dy.sh;
+        const uint4* xp = x.p + b * x.sb + s * x.ss + h0 * x.sh;
         uint4 vy[kQkBwdUnroll][2], vx[kQkBwdUnroll][2];
 #pragma unroll
         for (int u = 0; u < kQkBwdUnroll; ++u) {
-            const int h = h0 + u * rows;
             vy[u][0] = vy[u][1] = vx[u][0] = vx[u][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (works && h < H) {
-                vy[u][0] = load_once(yp + h * dy.sh + v0);
-                vy[u][1] = load_once(yp + h * dy.sh + v1);
-                vx[u][0] = load_once(xp + h * x.sh + v0);
-                vx[u][1] = load_once(xp + h * x.sh + v1);
+            if (works && h0 + u * rows < H) {
+                vy[u][0] = load_once(yp + u * rows * dy.sh + v0);
+                vy[u][1] = load_once(yp + u * rows * dy.sh + v1);
+                vx[u][0] = load_once(xp + u * rows * x.sh + v0);
+                vx[u][1] = load_once(xp + u * rows * x.sh + v1);
             }
         }
         const long long p = a.pos != nullptr ? a.pos[b * a.pos_stride + s] : s;
         const bool bad = p < 0 || p >= a.P;
-        if (bad && lane == 0) atomicExch(a.status, -1);
-        float c[8], sn[8];
-        if (works && !bad) qk_angles(a, p, slot, c, sn);
-        uint4* op = dx.p + b * dx.sb + s * dx.ss;
+        if (bad && lane == 0) atomicExch(a.status, kStatusBad);
+        const bool turns = slot < a.nrot && !bad;
+        QkPairs d[kQkBwdUnroll];
+        float both[2 * kQkBwdUnroll];
+        {
+            QkAngles ang{};
+            if (turns) ang = qk_angles(a, p, slot);
+#pragma unroll
+            for (int u = 0; u < kQkBwdUnroll; ++u) {
+                const QkPairs f = qk_widen<INTER>(vx[u][0], vx[u][1]);
+                d[u] = qk_widen<INTER>(vy[u][0], vy[u][1]);
+                if (turns) qk_rotate(d[u], ang);
+                both[2 * u] = qk_dot(f, f);
+                QkPairs e;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e.x[i] = f2_mul(d[u].x[i], g.x[i]), e.y[i] = f2_mul(d[u].y[i], g.y[i]);
+                both[2 * u + 1] = qk_dot(e, f);
+            }
+        }
+        group_sums(both, group);
+        uint4* op = dx.p + b * dx.sb + s * dx.ss + h0 * dx.sh;
 #pragma unroll
         for (int u = 0; u < kQkBwdUnroll; ++u) {
-            const int h = h0 + u * rows;
-            float f[2][8], d[2][8];
-            widen8(vx[u][0], f[0]);
-            widen8(vx[u][1], f[1]);
-            widen8(vy[u][0], d[0]);
-            widen8(vy[u][1], d[1]);
-            if (works && !bad && slot < a.nrot) qk_rotate<INTER>(d, c, sn);
-            float ss = 0.0f;
+            if (!works || h0 + u * rows >= H) continue;
+            const float r = rsqrtf(both[2 * u] * a.inv_d + a.eps);
+            // of x r: its products stay in range where x^2 does
+            const float m = -(both[2 * u + 1] * r * a.inv_d);
+            const uint64_t rr = f2_packf(r, r), mm = f2_packf(m, m);
+            const QkPairs f = qk_widen<INTER>(vx[u][0], vx[u][1]);
+            QkPairs o;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(f[0][i], f[0][i], fmaf(f[1][i], f[1][i], ss));
-            const float r = 1.0f / sqrtf(group_sum(ss, group) * a.inv_d + a.eps);
-            const bool store = works && h < H;
-            float dot = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    f[w][i] *= r;
-                    if (store && !bad) acc[w][i] = fmaf(d[w][i], f[w][i], acc[w][i]);
-                    d[w][i] *= g[w][i];
-                    dot = fmaf(d[w][i], f[w][i], dot);
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t hx = f2_mul(f.x[i], rr), hy = f2_mul(f.y[i], rr);
+                if (!bad) {
+                    acc.x[i] = f2_fma(d[u].x[i], hx, acc.x[i]);
+                    acc.y[i] = f2_fma(d[u].y[i], hy, acc.y[i]);
                 }
-            const float m = group_sum(dot, group) * a.inv_d;
-            if (!store) continue;
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[w][i] = r * (d[w][i] - f[w][i] * m);
-            op[h * dx.sh + v0] = bad ? qk_nan() : round8(d[0]);
-            op[h * dx.sh + v1] = bad ? qk_nan() : round8(d[1]);
+                o.x[i] = f2_mul(rr, f2_fma(hx, mm, f2_mul(d[u].x[i], g.x[i])));
+                o.y[i] = f2_mul(rr, f2_fma(hy, mm, f2_mul(d[u].y[i], g.y[i])));
+            }
+            uint4 o0, o1;
+            qk_round<INTER>(o, o0, o1);
+            op[u * rows * dx.sh + v0] = bad ? qk_nan() : o0;
+            op[u * rows * dx.sh + v1] = bad ? qk_nan() : o1;
         }
     }
     if (a.part == nullptr) return;
+    // a value's place among the 16 of its thread's two vectors
+    float sum[16];
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+    for (int i = 0; i < 4; ++i) {
+        const int x0 = INTER ? 4 * i : 2 * i, step = INTER ? 2 : 1, y0 = INTER ? 4 * i + 1 : 8 + 2 * i;
+        f2_unpack(acc.x[i], sum[x0], sum[x0 + step]);
+        f2_unpack(acc.y[i], sum[y0], sum[y0 + step]);
+    }
+    for (int o = group; o < 32; o <<= 1)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            for (int o = group; o < 32; o <<= 1) acc[w][i] += __shfl_xor_sync(0xffffffffu, acc[w][i], o);
+        for (int i = 0; i < 16; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
     if (lane < a.nslot) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            sums[warp][8 * v0 + i] = acc[0][i];
-            sums[warp][8 * v1 + i] = acc[1][i];
-        }
+        for (int i = 0; i < 16; ++i) sums[warp][8 * (i < 8 ? v0 : v1) + (i & 7)] = sum[i];
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.D; e += kQkThreads) {

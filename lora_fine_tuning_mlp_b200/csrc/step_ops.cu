@@ -451,7 +451,8 @@ int validate_qk(const lora_qk_shape* sh) {
     if (!std::isfinite(sh->eps) || sh->eps < 0.0f) return LORA_MLP_ERR_INVALID_ARG;
     if (sh->D % 16 || sh->rot % 16 || sh->D > 512) return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
     const int64_t lim = INT32_MAX;
-    if (sh->B > lim || sh->S > lim || sh->Hq > 65536 || sh->Hk > 65536 || sh->P > lim || sh->B * sh->S > lim)
+    if (sh->B > lim || sh->S > lim || sh->Hq > 65536 || sh->Hk > 65536 || sh->P > lim || sh->B * sh->S > lim ||
+        sh->B * sh->S * ((sh->Hq + 1) / 2 + (sh->Hk + 1) / 2) > lim)
         return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
     return LORA_MLP_OK;
 }
@@ -466,6 +467,11 @@ QkView qk_view(const lora_qk_view* v) {
     return {static_cast<uint4*>(v->data), v->stride_b / 8, v->stride_s / 8, v->stride_h / 8};
 }
 
+QkDivisor qk_divisor(int64_t d) {
+    const int l = ceil_log2(static_cast<uint64_t>(d));
+    return {static_cast<uint32_t>(d), static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << l) - d)) / d + 1), l};
+}
+
 QkArgs qk_args(const lora_qk_shape* sh, const void* q_gain, const void* k_gain, const float* cos, const float* sin,
                const int64_t* positions, int* status, int unroll) {
     QkArgs a{};
@@ -476,7 +482,7 @@ QkArgs qk_args(const lora_qk_shape* sh, const void* q_gain, const void* k_gain, 
     a.pos = reinterpret_cast<const long long*>(positions);
     a.pos_stride = sh->position_stride;
     a.T = sh->B * sh->S;
-    a.S = sh->S;
+    a.seq = qk_divisor(sh->S);
     a.P = sh->P;
     a.H[0] = static_cast<int>(sh->Hq);
     a.H[1] = static_cast<int>(sh->Hk);
@@ -491,6 +497,9 @@ QkArgs qk_args(const lora_qk_shape* sh, const void* q_gain, const void* k_gain, 
     a.status = status;
     const int heads = (32 >> a.log_group) * unroll;
     for (int i = 0; i < 2; ++i) a.units[i] = (a.H[i] + heads - 1) / heads;
+    a.per_query = qk_divisor(a.units[0]);
+    a.per_key = qk_divisor(a.units[1]);
+    a.per_token = qk_divisor(a.units[0] + a.units[1]);
     return a;
 }
 
@@ -498,7 +507,6 @@ QkArgs qk_args(const lora_qk_shape* sh, const void* q_gain, const void* k_gain, 
 int launch_qk(const char* name, const QkArgs& a, bool norm, bool inter, cudaStream_t st) {
     const int64_t units = a.T * (a.units[0] + a.units[1]);
     const int64_t blocks = (units + kQkWarps - 1) / kQkWarps;
-    if (blocks > INT32_MAX) return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
     auto kernel = norm ? (inter ? qk_rope_kernel<true, true> : qk_rope_kernel<true, false>)
                        : (inter ? qk_rope_kernel<false, true> : qk_rope_kernel<false, false>);
     return launch(name, kernel, dim3(static_cast<unsigned>(blocks)), kQkThreads, 0, st, false, 1, a);
@@ -506,7 +514,7 @@ int launch_qk(const char* name, const QkArgs& a, bool norm, bool inter, cudaStre
 
 // Blocks of the backward through the norm for queries and keys: together at
 // most kQkBwdBlocks, shared in proportion to their units.
-constexpr int64_t kQkBwdBlocks = 148 * 5;
+constexpr int64_t kQkBwdBlocks = 148 * kQkBwdBlocksPerSm;
 
 void qk_bwd_blocks(const QkArgs& a, int64_t (&blocks)[2]) {
     const int64_t uq = a.T * a.units[0], uk = a.T * a.units[1];
@@ -533,7 +541,8 @@ int lora_qk_rope_forward(const lora_qk_shape* shape, const lora_qk_view* q, cons
                            {k_gain, 16}, {cos, 16}, {sin, 16}, {positions, 8}}));
     DevInfo di;
     STEP_TRY(device_info(&di));
-    QkArgs a = qk_args(shape, q_gain, k_gain, cos, sin, positions, di.status, kQkUnroll);
+    QkArgs a = qk_args(shape, q_gain, k_gain, cos, sin, positions, di.status,
+                       q_gain != nullptr ? kQkUnroll : kQkRopeUnroll);
     a.in[0] = qk_view(q);
     a.in[1] = qk_view(k);
     a.out[0] = qk_view(q_out);
@@ -573,7 +582,7 @@ int lora_qk_rope_backward(const lora_qk_shape* shape, const lora_qk_view* q, con
     DevInfo di;
     STEP_TRY(device_info(&di));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    QkArgs a = qk_args(shape, q_gain, k_gain, cos, sin, positions, di.status, norm ? kQkBwdUnroll : kQkUnroll);
+    QkArgs a = qk_args(shape, q_gain, k_gain, cos, sin, positions, di.status, norm ? kQkBwdUnroll : kQkRopeUnroll);
     a.in[0] = qk_view(dq_out);
     a.in[1] = qk_view(dk_out);
     a.out[0] = qk_view(dq);
