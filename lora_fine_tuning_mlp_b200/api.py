@@ -146,6 +146,16 @@ class Workspace:
         return self.buf
 
 
+def _scratch(workspace, nbytes: int, device, stream):
+    """The workspace's buffer, or one for this call alone, which the allocator then keeps for `stream` too."""
+    if workspace is not None:
+        return workspace.get(nbytes, device)
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        buf.record_stream(stream)
+    return buf
+
+
 def sizes(w: MLPWeights, N: int):
     """(forward workspace, backward workspace, saved) byte counts."""
     return _lib.sizes(w.shape(N))
@@ -780,7 +790,7 @@ def embedding_backward(dOut: torch.Tensor, ids: torch.Tensor, V: int, *, scale: 
         raise ValueError(f"padding_idx must be in [0, {V})")
     dev = dOut.device
     dE = torch.empty((V, d), dtype=dtype, device=dev) if dE is None else _need(dE, "dE", dtype, (V, d))
-    ws = (workspace or Workspace()).get(_lib.embedding_sizes(N, V, d), dev)
+    ws = _scratch(workspace, _lib.embedding_sizes(N, V, d), dev, stream)
     _lib.check(_lib.embedding_backward(N, V, d, scale, -1 if padding_idx is None else padding_idx, kind, _p(ids),
                                        _p(dOut), _p(dE), _p(ws), ws.numel(), _stream(stream)),
                "lora_embedding_backward")
@@ -919,7 +929,7 @@ def qk_norm_rope_backward(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, s
     dgq = dgk = ws = None
     if q_gain is not None and gain_grads:
         dgq, dgk = q.new_empty((2, shape.D), dtype=torch.float32).unbind(0)
-        ws = (workspace or Workspace()).get(_lib.qk_rope_sizes(shape), q.device)
+        ws = _scratch(workspace, _lib.qk_rope_sizes(shape), q.device, stream)
     _lib.check(_lib.qk_rope_backward(shape, vq, vk, *rest, vdq_out, vdk_out, vdq, vdk, _p(dgq), _p(dgk), _p(ws),
                                      0 if ws is None else ws.numel(), _stream(stream)), "lora_qk_rope_backward")
     return dq, dk, dgq, dgk
@@ -1041,7 +1051,7 @@ def distill_loss(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ids
                                 ignore_index)
     out = logits.new_empty((2,), dtype=torch.float32)
     dlogits = _distill_out(logits, grad_out, inplace) if with_grad else None
-    ws = (workspace or Workspace()).get(_lib.distill_sizes(shape), logits.device)
+    ws = _scratch(workspace, _lib.distill_sizes(shape), logits.device, stream)
     _lib.check(_lib.distill_loss(shape, *ptrs, red, _p(out), _p(dlogits), _p(ws), ws.numel(), _stream(stream)),
                "lora_distill_loss")
     return out, dlogits
@@ -1099,6 +1109,7 @@ class DistillFunction(torch.autograd.Function):
 
 
 def step_device_status(stream=None) -> int:
-    """Reads and clears the device-side status of the operators around the dense layers (embedding, norm and rotation of queries and
-    keys, distillation): 0, or _lib.ERR_INVALID_ARG after an id or position outside its range.  Synchronises the stream."""
+    """Reads and clears the device-side status of the operators around the dense layers (embedding, norm and rotation
+    of queries and keys, distillation): 0, _lib.ERR_INVALID_ARG after an id or position outside its range, or
+    _lib.ERR_DEVICE_TIMEOUT after a wait between blocks that ran out.  Synchronises the stream."""
     return _lib.step_device_status(_stream(stream))

@@ -93,6 +93,10 @@ def check_grad(dOut, ids, V, scale, dtype, padding_idx, got):
     ("heavy", 30000, 2, 64),
     ("zipf", 9000, 300007, 32),  # ids of 19 bits: three passes
     ("uniform", 700, 270001, 8),
+    ("zipf", 1500, 900, 16),     # two and four tokens a thread of the one block's sort
+    ("heavy", 3000, 70, 24),
+    ("zipf", 140001, 3001, 8),   # wider tiles of the many-block sort
+    ("heavy", 40000, 300, 1032), # more chunks than blocks are worth: wider slices
 ])
 def test_gradient(kind, N, V, d, dtype):
     rng = np.random.default_rng(N * 7 + V)
