@@ -31,6 +31,9 @@
  * gives the same bits; a row's last bits may depend on the rows beside it.
  * Other conventions: lora_step.h.
  *
+ * The quotients 1 / T and s / T (with softcapping cap / T and s / cap) must stay
+ * below 10^37.
+ *
  * A teacher id below -1 or not below V is a device-side finding: the entry
  * counts as absent, the row's loss is NaN, and lora_step_device_status reports
  * LORA_MLP_ERR_INVALID_ARG.  LORA_MLP_ERR_DEVICE_TIMEOUT there means that a

@@ -7,7 +7,9 @@
  * every pointer is caller-owned device memory of the current device; all work
  * is enqueued on `stream` (a cudaStream_t, NULL = legacy default stream);
  * nothing is allocated or synchronised; argument errors are found on the host
- * before anything is enqueued; results are bitwise deterministic.
+ * before anything is enqueued; results are bitwise deterministic.  A workspace
+ * belongs to one call at a time: calls (or captured graphs) that may run at
+ * once on several streams need one each.
  */
 #ifndef LORA_STEP_H
 #define LORA_STEP_H
@@ -24,7 +26,8 @@ extern "C" {
 /* Reads and clears the device-side status of these operators on the current
  * device: LORA_MLP_OK, or LORA_MLP_ERR_INVALID_ARG after a token id, position
  * or teacher id outside its range (each header says what such an entry's
- * result is).  Synchronises `stream`. */
+ * result is), or LORA_MLP_ERR_DEVICE_TIMEOUT after a bounded wait between
+ * blocks ran out (lora_distill.h).  Synchronises `stream`. */
 int lora_step_device_status(void* stream, int* status);
 
 /* Kernel timing of these operators, as lora_mlp_timing_enable and

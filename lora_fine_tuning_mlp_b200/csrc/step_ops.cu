@@ -619,6 +619,10 @@ int validate_distill(const lora_distill_shape* sh) {
     if (!std::isfinite(sh->temperature) || !(sh->temperature > 0.0f)) return LORA_MLP_ERR_INVALID_ARG;
     if (!std::isfinite(sh->logit_scale) || sh->logit_scale == 0.0f) return LORA_MLP_ERR_INVALID_ARG;
     if (!std::isfinite(sh->softcap) || sh->softcap < 0.0f) return LORA_MLP_ERR_INVALID_ARG;
+    // the kernel's factors of an exponent, and of the teacher's
+    const double T = sh->temperature, cap = sh->softcap, scale = std::fabs(static_cast<double>(sh->logit_scale));
+    const double unit = cap > 0.0 ? std::max(2.0 * cap / T, 2.0 * scale / cap) : scale / T;
+    if (!(std::max(unit, 1.0 / T) < 1e38)) return LORA_MLP_ERR_INVALID_ARG;
     if (sh->values_type != LORA_DISTILL_VALUES_BF16 && sh->values_type != LORA_DISTILL_VALUES_FP32)
         return LORA_MLP_ERR_INVALID_ARG;
     if (sh->ids_type != LORA_DISTILL_IDS_INT32 && sh->ids_type != LORA_DISTILL_IDS_INT64)

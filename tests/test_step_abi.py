@@ -159,6 +159,9 @@ def ds_shape(N=4, V=100, ld=104, K=8, T=1.0, s=1.0, cap=0.0, vt=1, it=1):
     (dict(ld=96), _lib.ERR_INVALID_ARG),
     (dict(T=0.0), _lib.ERR_INVALID_ARG),
     (dict(T=-1.0), _lib.ERR_INVALID_ARG),
+    (dict(T=1e-39), _lib.ERR_INVALID_ARG),           # 1 / T is out of fp32's range
+    (dict(cap=1e-39), _lib.ERR_INVALID_ARG),
+    (dict(s=1e20, T=1e-20), _lib.ERR_INVALID_ARG),
     (dict(T=float("inf")), _lib.ERR_INVALID_ARG),
     (dict(s=0.0), _lib.ERR_INVALID_ARG),
     (dict(cap=-2.0), _lib.ERR_INVALID_ARG),
