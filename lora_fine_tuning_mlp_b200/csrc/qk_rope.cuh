@@ -51,15 +51,17 @@ struct QkArgs {
     const long long* pos;
     long long pos_stride;
     long long T, P;
-    QkDivisor seq;                              // S
-    QkDivisor per_token, per_query, per_key;    // a token's units
+    QkDivisor seq;        // S
+    QkDivisor by[2];      // a token's units of queries, of keys; flat: its heads
+    QkDivisor per_token;  // its units
+    int flat;
     int H[2];
     int D, nslot, nrot, half;  // nslot = D/16 threads of a head do work, nrot = rot/16 of them turn pairs
     int log_group;
     float eps, inv_d;
     float turn;       // +1, or -1 to turn back
     int* status;
-    int units[2];     // of a token: ceil(heads / heads of a unit)
+    uint32_t units[2];  // of queries, of keys
     int blocks_q;     // backward: blocks [0, blocks_q) take queries, the others keys
     float* part;      // backward: [blocks][D] sums of dn xh, or null
 };
@@ -177,49 +179,88 @@ __device__ __forceinline__ void group_sums(float (&v)[N], int group) {
 
 __device__ __forceinline__ uint4 qk_nan() { return make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u); }
 
-// A warp's unit: one token and U * (32 / group) heads of its queries
-// or of its keys.
-template <bool NORM, bool INTER>
+// The token and the head that are row u of a unit for this lane; `in` if there
+// is one.  A unit is U * (32 / group) heads of one token, or, where half of that
+// and more would be empty (FLAT), of several tokens in a row: then each row has
+// angles of its own to read.
+template <bool FLAT>
+struct QkPlace {
+    uint32_t b, s;
+    int h;
+    bool in;
+    __device__ __forceinline__ uint4* head(const QkView& v) const { return v.p + b * v.sb + s * v.ss + h * v.sh; }
+    __device__ __forceinline__ long long position(const QkArgs& a) const {
+        return a.pos == nullptr ? s : !FLAT || in ? a.pos[b * a.pos_stride + s] : 0;
+    }
+};
+template <bool FLAT, int U>
+__device__ __forceinline__ QkPlace<FLAT> qk_place(const QkArgs& a, const QkDivisor& by, int H, uint32_t unit, int u) {
+    const uint32_t rows = 32u >> a.log_group, row = (threadIdx.x & 31) >> a.log_group;
+    const uint32_t item = FLAT ? (unit * U + u) * rows + row : unit;  // `by`: a token's heads, or its units
+    const uint32_t t = by.quotient(item), rest = item - t * by.d;
+    QkPlace<FLAT> l;
+    l.h = static_cast<int>(FLAT ? rest : (rest * U + u) * rows + row);
+    l.in = FLAT ? t < a.T : l.h < H;
+    l.b = a.seq.quotient(t);
+    l.s = t - l.b * a.seq.d;
+    return l;
+}
+
+// A warp takes a unit of queries or of keys.
+template <bool NORM, bool INTER, bool FLAT>
 __global__ void __launch_bounds__(kQkThreads, NORM ? 4 : 8) qk_rope_kernel(const QkArgs a) {
     constexpr int U = NORM ? kQkUnroll : kQkRopeUnroll;
-    const uint32_t unit = blockIdx.x * kQkWarps + (threadIdx.x >> 5);
-    const uint32_t t = a.per_token.quotient(unit);
-    if (t >= a.T) return;
-    int chunk = static_cast<int>(unit - t * a.per_token.d);
-    const int kind = chunk >= a.units[0];
-    if (kind) chunk -= a.units[0];
+    uint32_t unit = blockIdx.x * kQkWarps + (threadIdx.x >> 5);
+    int kind;
+    if (FLAT) {
+        kind = unit >= a.units[0];
+        if (kind) unit -= a.units[0];
+        if (unit >= a.units[kind]) return;
+    } else {  // a token's queries, then its keys
+        const uint32_t t = a.per_token.quotient(unit);
+        if (t >= a.T) return;
+        unit -= t * a.per_token.d;
+        kind = unit >= a.by[0].d;
+        unit = kind ? t * a.by[1].d + unit - a.by[0].d : t * a.by[0].d + unit;
+    }
     const int lane = threadIdx.x & 31, group = 1 << a.log_group, slot = lane & (group - 1);
-    const uint32_t b = a.seq.quotient(t), s = t - b * a.seq.d;
     const QkView in = kind ? a.in[1] : a.in[0], out = kind ? a.out[1] : a.out[0];
+    const QkDivisor by = kind ? a.by[1] : a.by[0];
     const int H = kind ? a.H[1] : a.H[0];
-    const int rows = 32 >> a.log_group;
-    const int h0 = chunk * rows * U + (lane >> a.log_group);
     const bool works = slot < a.nslot;
     int v0, v1;
     qk_vectors<INTER>(a, slot, v0, v1);
-    const uint4* ip = in.p + b * in.sb + s * in.ss + h0 * in.sh;
-    const long long next = rows * in.sh;
+    const int rows = 32 >> a.log_group;
+    const QkPlace<FLAT> l0 = qk_place<FLAT, U>(a, by, H, unit, 0);
     uint4 v[U][2];
+    long long p[FLAT ? U : 1];
+    const uint4* ip = l0.head(in);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        QkPlace<FLAT> l = l0;
+        if (FLAT && u > 0) l = qk_place<FLAT, U>(a, by, H, unit, u), ip = l.head(in);
         v[u][0] = v[u][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (works && h0 + u * rows < H) {
+        if (works && (FLAT ? l.in : l0.h + u * rows < H)) {
             v[u][0] = load_once(ip + v0);
             v[u][1] = load_once(ip + v1);
         }
-        ip += next;
+        if (!FLAT) ip += rows * in.sh;
+        if (FLAT || u == 0) p[FLAT ? u : 0] = l.position(a);
     }
     QkPairs g{};
     if (NORM && works) {
         const uint4* gp = kind ? a.gain[1] : a.gain[0];
         g = qk_widen<INTER>(__ldg(gp + v0), __ldg(gp + v1));
     }
-    const long long p = a.pos != nullptr ? a.pos[b * a.pos_stride + s] : s;
-    const bool bad = p < 0 || p >= a.P;
-    if (bad && lane == 0) atomicExch(a.status, kStatusBad);
-    const bool turns = slot < a.nrot && !bad;
+    bool bad = false, turns = false;
     QkAngles ang{};
-    if (turns) ang = qk_angles(a, p, slot);
+    const auto angles = [&](long long at) {
+        bad = at < 0 || at >= a.P;
+        if (bad && slot == 0) atomicExch(a.status, kStatusBad);
+        turns = slot < a.nrot && !bad;
+        if (turns) ang = qk_angles(a, at, slot);
+    };
+    angles(p[0]);
     float ss[U];
     if (NORM) {
 #pragma unroll
@@ -229,10 +270,15 @@ __global__ void __launch_bounds__(kQkThreads, NORM ? 4 : 8) qk_rope_kernel(const
         }
         group_sums(ss, group);
     }
-    uint4* op = out.p + b * out.sb + s * out.ss + h0 * out.sh;
-    const long long out_next = rows * out.sh;
+    uint4* op = l0.head(out);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        QkPlace<FLAT> l = l0;
+        if (FLAT && u > 0) {
+            angles(p[u]);
+            l = qk_place<FLAT, U>(a, by, H, unit, u);
+            op = l.head(out);
+        }
         QkPairs f = qk_widen<INTER>(v[u][0], v[u][1]);
         if (NORM) {
             const float r = rsqrtf(ss[u] * a.inv_d + a.eps);
@@ -244,13 +290,13 @@ __global__ void __launch_bounds__(kQkThreads, NORM ? 4 : 8) qk_rope_kernel(const
             }
         }
         if (turns) qk_rotate(f, ang);
-        if (works && h0 + u * rows < H) {
+        if (works && (FLAT ? l.in : l0.h + u * rows < H)) {
             uint4 o0, o1;
             qk_round<INTER>(f, o0, o1);
             op[v0] = bad ? qk_nan() : o0;
             op[v1] = bad ? qk_nan() : o1;
         }
-        op += out_next;
+        if (!FLAT) op += rows * out.sh;
     }
 }
 
@@ -261,17 +307,18 @@ __global__ void __launch_bounds__(kQkThreads, NORM ? 4 : 8) qk_rope_kernel(const
 // block's sums go to `part`, which qk_gain_kernel adds up in block order.
 constexpr int kQkBwdUnroll = 2;
 
-template <bool INTER>
+template <bool INTER, bool FLAT>
 __global__ void __launch_bounds__(kQkThreads, kQkBwdBlocksPerSm) qk_rope_bwd_kernel(const QkArgs a) {
     __shared__ float sums[kQkWarps][512];
     const int kind = static_cast<int>(blockIdx.x) >= a.blocks_q;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = 1 << a.log_group, slot = lane & (group - 1), rows = 32 >> a.log_group;
+    const int group = 1 << a.log_group, slot = lane & (group - 1);
     const uint32_t nblocks = kind ? gridDim.x - a.blocks_q : a.blocks_q;
     const uint32_t first = (kind ? blockIdx.x - a.blocks_q : blockIdx.x) * kQkWarps + warp;
     const QkView dy = kind ? a.in[1] : a.in[0], dx = kind ? a.out[1] : a.out[0], x = kind ? a.x[1] : a.x[0];
     const int H = kind ? a.H[1] : a.H[0];
-    const QkDivisor per_token = kind ? a.per_key : a.per_query;
+    const QkDivisor by = kind ? a.by[1] : a.by[0];
+    constexpr int U = kQkBwdUnroll;
     const bool works = slot < a.nslot;
     int v0, v1;
     qk_vectors<INTER>(a, slot, v0, v1);
@@ -281,38 +328,41 @@ __global__ void __launch_bounds__(kQkThreads, kQkBwdBlocksPerSm) qk_rope_bwd_ker
         g = qk_widen<INTER>(__ldg(gp + v0), __ldg(gp + v1));
     }
     let_next();
-    const uint32_t units = static_cast<uint32_t>(a.T) * per_token.d;
+    const uint32_t units = kind ? a.units[1] : a.units[0];
     for (uint32_t unit = first; unit < units; unit += nblocks * kQkWarps) {
-        const uint32_t t = per_token.quotient(unit), chunk = unit - t * per_token.d;
-        const uint32_t b = a.seq.quotient(t), s = t - b * a.seq.d;
-        const int h0 = static_cast<int>(chunk) * rows * kQkBwdUnroll + (lane >> a.log_group);
-        const uint4* yp = dy.p + b * dy.sb + s * dy.ss + h0 * dy.sh;
-        const uint4* xp = x.p + b * x.sb + s * x.ss + h0 * x.sh;
-        uint4 vy[kQkBwdUnroll][2], vx[kQkBwdUnroll][2];
+        uint4 vy[U][2], vx[U][2];
+        long long p[FLAT ? U : 1];
+        QkPlace<FLAT> l[U];
 #pragma unroll
-        for (int u = 0; u < kQkBwdUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
+            l[u] = qk_place<FLAT, U>(a, by, H, unit, u);
             vy[u][0] = vy[u][1] = vx[u][0] = vx[u][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (works && h0 + u * rows < H) {
-                vy[u][0] = load_once(yp + u * rows * dy.sh + v0);
-                vy[u][1] = load_once(yp + u * rows * dy.sh + v1);
-                vx[u][0] = load_once(xp + u * rows * x.sh + v0);
-                vx[u][1] = load_once(xp + u * rows * x.sh + v1);
+            if (works && l[u].in) {
+                const uint4 *yp = l[u].head(dy), *xp = l[u].head(x);
+                vy[u][0] = load_once(yp + v0);
+                vy[u][1] = load_once(yp + v1);
+                vx[u][0] = load_once(xp + v0);
+                vx[u][1] = load_once(xp + v1);
             }
+            if (FLAT || u == 0) p[FLAT ? u : 0] = l[u].position(a);
         }
-        const long long p = a.pos != nullptr ? a.pos[b * a.pos_stride + s] : s;
-        const bool bad = p < 0 || p >= a.P;
-        if (bad && lane == 0) atomicExch(a.status, kStatusBad);
-        const bool turns = slot < a.nrot && !bad;
-        QkPairs d[kQkBwdUnroll];
-        float both[2 * kQkBwdUnroll];
+        bool bad[U];
+        QkPairs d[U];
+        float both[2 * U];
         {
             QkAngles ang{};
-            if (turns) ang = qk_angles(a, p, slot);
 #pragma unroll
-            for (int u = 0; u < kQkBwdUnroll; ++u) {
+            for (int u = 0; u < U; ++u) {
+                if (FLAT || u == 0) {
+                    bad[u] = p[u] < 0 || p[u] >= a.P;
+                    if (bad[u] && slot == 0) atomicExch(a.status, kStatusBad);
+                    if (slot < a.nrot && !bad[u]) ang = qk_angles(a, p[u], slot);
+                } else {
+                    bad[u] = bad[0];
+                }
                 const QkPairs f = qk_widen<INTER>(vx[u][0], vx[u][1]);
                 d[u] = qk_widen<INTER>(vy[u][0], vy[u][1]);
-                if (turns) qk_rotate(d[u], ang);
+                if (slot < a.nrot && !bad[u]) qk_rotate(d[u], ang);
                 both[2 * u] = qk_dot(f, f);
                 QkPairs e;
 #pragma unroll
@@ -321,10 +371,9 @@ __global__ void __launch_bounds__(kQkThreads, kQkBwdBlocksPerSm) qk_rope_bwd_ker
             }
         }
         group_sums(both, group);
-        uint4* op = dx.p + b * dx.sb + s * dx.ss + h0 * dx.sh;
 #pragma unroll
-        for (int u = 0; u < kQkBwdUnroll; ++u) {
-            if (!works || h0 + u * rows >= H) continue;
+        for (int u = 0; u < U; ++u) {
+            if (!works || !l[u].in) continue;
             const float r = rsqrtf(both[2 * u] * a.inv_d + a.eps);
             // of x r: its products stay in range where x^2 does
             const float m = -(both[2 * u + 1] * r * a.inv_d);
@@ -334,17 +383,17 @@ __global__ void __launch_bounds__(kQkThreads, kQkBwdBlocksPerSm) qk_rope_bwd_ker
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint64_t hx = f2_mul(f.x[i], rr), hy = f2_mul(f.y[i], rr);
-                if (!bad) {
+                if (!bad[u]) {
                     acc.x[i] = f2_fma(d[u].x[i], hx, acc.x[i]);
                     acc.y[i] = f2_fma(d[u].y[i], hy, acc.y[i]);
                 }
                 o.x[i] = f2_mul(rr, f2_fma(hx, mm, f2_mul(d[u].x[i], g.x[i])));
                 o.y[i] = f2_mul(rr, f2_fma(hy, mm, f2_mul(d[u].y[i], g.y[i])));
             }
-            uint4 o0, o1;
+            uint4 o0, o1, *op = l[u].head(dx);
             qk_round<INTER>(o, o0, o1);
-            op[u * rows * dx.sh + v0] = bad ? qk_nan() : o0;
-            op[u * rows * dx.sh + v1] = bad ? qk_nan() : o1;
+            op[v0] = bad[u] ? qk_nan() : o0;
+            op[v1] = bad[u] ? qk_nan() : o1;
         }
     }
     if (a.part == nullptr) return;

@@ -91,6 +91,8 @@ CASES = [
     (1, 33, 3, 2, 512, 512, False, "packed"), # a head a warp
     (1, 5, 70, 1, 32, 16, True, "bshd"),      # more heads than a unit
     (4, 300, 6, 2, 48, 32, False, "bshd"),
+    (5, 211, 1, 1, 128, 128, False, "packed"),  # units of several tokens, across sequences
+    (2, 61, 40, 9, 64, 64, True, "bshd"),     # units of one token, the last of them partly empty
 ]
 
 
@@ -210,6 +212,20 @@ def test_bad_positions_are_reported_and_stay_in_their_tokens():
         assert torch.equal(a[:, keep], b[:, keep]) and torch.all(torch.isnan(a[:, ~keep]))
     assert torch.all(torch.isnan(dq[:, ~keep])) and torch.all(torch.isfinite(dq[:, keep]))
     assert torch.all(torch.isfinite(dgq)) and torch.all(torch.isfinite(dgk))
+
+
+def test_bad_positions_among_many_heads():
+    rng = np.random.default_rng(16)
+    S, D = 5, 64
+    q, k = heads(rng, "bshd", 1, S, 48, D), heads(rng, "bshd", 1, S, 32, D)
+    cos, sin = api.rope_table(S, D, device="cuda")
+    pos = torch.arange(S, device="cuda")
+    ref = api.qk_norm_rope_forward(q, k, cos, sin, positions=pos)
+    pos[3] = 2 ** 40
+    got = api.qk_norm_rope_forward(q, k, cos, sin, positions=pos)
+    assert api.step_device_status() == _lib.ERR_INVALID_ARG and api.step_device_status() == 0
+    for a, b in zip(got, ref):
+        assert torch.equal(a[:, :3], b[:, :3]) and torch.equal(a[:, 4], b[:, 4]) and torch.all(torch.isnan(a[:, 3]))
 
 
 def test_zero_heads_and_infinities_stay_apart():
