@@ -164,7 +164,8 @@ const char* lora_mlp_strerror(int code);
  * of the library is bracketed by a pair of CUDA events on its stream.
  * lora_mlp_timing_collect synchronises those events, writes up to `max`
  * (name, milliseconds) records in launch order, returns how many were
- * recorded in *count, and clears the record.  Names are static strings. */
+ * recorded in *count, and clears the record.  Names are static strings.
+ * (The operators of lora_step.h have their own record, and their own count.) */
 typedef struct lora_mlp_kernel_time {
     const char* name;
     float ms;

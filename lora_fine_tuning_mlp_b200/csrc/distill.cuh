@@ -32,6 +32,11 @@
 // = cap - 2 cap r with r = 1 / (1 + 2^(cap2 z)): exponents are taken of -r,
 // dt/dz = 4 s r (1 - r) has no cancellation where tanh saturates, and four
 // logits share one reciprocal.
+//
+// On a B200: 4096 rows of 128256 logits, loss and gradient, 454 us (4.6 TB/s; the
+// same stream of chunks merely copied takes 390, the exponentials' unit 248); the
+// loss of 2047 rows alone 106 us (4.9 TB/s); 1024 rows of 256000 with softcapping
+// 418 us, bound by the same unit's four operations a logit.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -415,7 +420,9 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
     const long long c0 = static_cast<long long>(rank) * a.slice;
     const int n = static_cast<int>(max(0LL, min(static_cast<long long>(a.slice), a.V - c0)));  // this block's logits
     const int nfull = n >> 3, ntail = n & 7;
-    // every chunk has `chunk` vectors but the slice's last
+    // every chunk has `chunk` vectors but the slice's last, also in the cluster's
+    // last slice: it is shorter by 64 logits at most, and chunks are longer where
+    // there are several
     const int chunk = a.chunk, end = a.chunks - 1, rest = nfull - end * chunk;
     uint4* ring = reinterpret_cast<uint4*>(raw);
     float* entries = reinterpret_cast<float*>(ring + a.slots * a.chunk);

@@ -10,9 +10,14 @@
 // its own: vectors j and j + rot/16 for pairs (i, i + rot/2), vectors 2j and
 // 2j + 1 for neighbouring pairs; behind `rot`, neighbouring vectors.  D/16
 // threads (rounded up to a power of two, `group`) make up a head, and a warp
-// works on 32/group heads of one token at a time, kQkUnroll times over, so
-// that the token's angles and the gains are read once for all of them and
-// every load of a thread is in flight before the first is used.
+// works on 32/group heads at a time, several times over, so that a token's
+// angles and the gains are read once for all of them and every load of a thread
+// is in flight before the first is used.
+//
+// On a B200, 4096 tokens of 32 + 8 heads of 128: forward 20 us, backward 35 and
+// 6 for the gains' sums, bound by the latency of their instructions at the few
+// warps that their registers allow; 32768 tokens of 32 + 4 heads of 64 without
+// the norm: 54 us a pass, 5.6 TB/s.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
