@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kZeroThreads) embed_zero_kernel(uint4* out, lo
     const long long i = static_cast<long long>(blockIdx.x) * kZeroBlock + threadIdx.x;
 #pragma unroll
     for (int k = 0; k < kZeroStores; ++k)
-        if (i + k * kZeroThreads < n) out[i + k * kZeroThreads] = make_uint4(0u, 0u, 0u, 0u);
+        if (i + k * kZeroThreads < n) __stcs(out + i + k * kZeroThreads, make_uint4(0u, 0u, 0u, 0u));
     // nothing here needs the sort, but who waits for this kernel relies on it
     if (blockIdx.x == gridDim.x - 1) wait_prior();
 }
@@ -421,10 +421,10 @@ __device__ __forceinline__ void store_grad(const EmbBwdArgs& a, uint32_t row, in
         const long long at = static_cast<long long>(row) * a.nv + j + h * step;
         if (F32) {
             float4* o = reinterpret_cast<float4*>(a.dE) + 2 * at;
-            o[0] = make_float4(acc[h][0], acc[h][1], acc[h][2], acc[h][3]);
-            o[1] = make_float4(acc[h][4], acc[h][5], acc[h][6], acc[h][7]);
+            __stcs(o, make_float4(acc[h][0], acc[h][1], acc[h][2], acc[h][3]));
+            __stcs(o + 1, make_float4(acc[h][4], acc[h][5], acc[h][6], acc[h][7]));
         } else {
-            reinterpret_cast<uint4*>(a.dE)[at] = round8(acc[h]);
+            __stcs(reinterpret_cast<uint4*>(a.dE) + at, round8(acc[h]));
         }
     }
 }

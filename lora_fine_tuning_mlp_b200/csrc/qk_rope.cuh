@@ -298,8 +298,8 @@ __global__ void __launch_bounds__(kQkThreads, NORM ? 4 : 8) qk_rope_kernel(const
         if (works && (FLAT ? l.in : l0.h + u * rows < H)) {
             uint4 o0, o1;
             qk_round<INTER>(f, o0, o1);
-            op[v0] = bad ? qk_nan() : o0;
-            op[v1] = bad ? qk_nan() : o1;
+            __stcs(op + v0, bad ? qk_nan() : o0);
+            __stcs(op + v1, bad ? qk_nan() : o1);
         }
         if (!FLAT) op += rows * out.sh;
     }
@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(kQkThreads, kQkBwdBlocksPerSm) qk_rope_bwd_ker
             }
             uint4 o0, o1, *op = l[u].head(dx);
             qk_round<INTER>(o, o0, o1);
-            op[v0] = bad[u] ? qk_nan() : o0;
-            op[v1] = bad[u] ? qk_nan() : o1;
+            __stcs(op + v0, bad[u] ? qk_nan() : o0);
+            __stcs(op + v1, bad[u] ? qk_nan() : o1);
         }
     }
     if (a.part == nullptr) return;

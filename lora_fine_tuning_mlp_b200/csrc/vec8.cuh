@@ -27,8 +27,17 @@ __device__ __forceinline__ uint4 round8(const float (&f)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 16 bytes that this launch reads once.
-__device__ __forceinline__ uint4 load_once(const void* p) { return __ldcs(static_cast<const uint4*>(p)); }
+// 16 bytes that this launch reads once and nobody writes meanwhile: not kept in
+// L1, and written results (__stcs) leave L2 first.  32768 tokens of 32 + 4 heads
+// turned both ways take 103 us so, 116 with a streaming load (ld.cs), 109 with
+// plain stores.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 
 // The kernel before this one in the stream has ended and its writes are
 // visible (programmatic dependent launch; nothing to wait for otherwise).
