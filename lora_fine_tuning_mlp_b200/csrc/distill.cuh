@@ -23,12 +23,17 @@
 // One exponential a logit and pass is what the special-function unit can
 // deliver in about the time that HBM takes, so the passes do little else.  In
 // particular they look for no maximum: sums are taken relative to a reference
-// m that stays from row to row (0 at first), 2^(z k - m k) with one fma.  A row
-// whose sum leaves the middle of fp32's range (its largest logit far from m,
-// infinities, a vocabulary masked whole) is summed again, after a search for
-// its maximum, which is the reference from then on; where m k itself is out of
-// fma's range the difference z - m is formed first.  Either way the result is
-// the softmax to fp32's precision.  With softcapping, t = cap tanh(s z / cap)
+// m that stays from row to row (0 at first), 2^(z k - E) with one fma, E = fl(m
+// k).  A row whose sum leaves the middle of fp32's range (its largest logit far
+// from m, infinities, a vocabulary masked whole) is summed again, after a
+// search for its maximum, which is the reference from then on.  E's rounding is
+// in the row's sum as in its terms and leaves no trace in the softmax, as long
+// as it is small itself: from |E| = 2^20 on (logits of 10^6, a temperature of
+// 10^-6) exponents are formed of the difference z - m, and the reference is not
+// kept for other rows.  Either way an exponent is off by 2^-23 of its distance
+// from the reference, which is fp32's own precision of it.
+//
+// With softcapping, t = cap tanh(s z / cap)
 // = cap - 2 cap r with r = 1 / (1 + 2^(cap2 z)): exponents are taken of -r,
 // dt/dz = 4 s r (1 - r) has no cancellation where tanh saturates, and four
 // logits share one reciprocal.
@@ -149,15 +154,24 @@ __device__ __forceinline__ float ds_warp_sum(float v) {
 // References m are kept as sign * z (as -r with softcapping), so that more is
 // more whatever the sign of k; |k| m is their exponent.
 __device__ __forceinline__ float ds_exponent(const DsArgs& a, float m) { return __fmul_rn(m, fabsf(a.k)); }
-// Whether it is out of the range in which x k - fl(|k| m) is formed by one fma.
+// Whether it is so large that its rounding alone (2^-24 of it) shifts the sums
+// of a row by a part that counts: at 2^20 a sixteenth of a power of two, at
+// 2^32 out of fp32.
+constexpr float kDsFar = 0x1p20f;
+__device__ __forceinline__ bool ds_far(const DsArgs& a, float m) { return !(fabsf(ds_exponent(a, m)) < kDsFar); }
+// m as what exponents are taken of.
 template <bool CAP>
-__device__ __forceinline__ bool ds_far(const DsArgs& a, float m) {
-    return !CAP && !(fabsf(ds_exponent(a, m)) < 1.0e30f);
+__device__ __forceinline__ float ds_origin(const DsArgs& a, float m) {
+    return CAP ? m : a.sign * m;
 }
-// A term of a sum that is relative to m.
+// The exponent of a term of a sum that is relative to m.
+template <bool CAP>
+__device__ __forceinline__ float ds_power(const DsArgs& a, float x, float m) {
+    return ds_far(a, m) ? (x - ds_origin<CAP>(a, m)) * a.k : fmaf(x, a.k, -ds_exponent(a, m));
+}
 template <bool CAP>
 __device__ __forceinline__ float ds_rel(const DsArgs& a, float x, float m) {
-    return ds_far<CAP>(a, m) ? ds_ex2((x - a.sign * m) * a.k) : ds_ex2(fmaf(x, a.k, -ds_exponent(a, m)));
+    return ds_ex2(ds_power<CAP>(a, x, m));
 }
 
 // The warps of a cluster that work on its slices tell one another a number
@@ -324,9 +338,11 @@ __device__ __forceinline__ void ds_add8(const DsArgs& a, const float (&x)[8], fl
 }
 
 // The gradient of a vector, the teacher's part left out: g / s 2^(x k - |k| m)
-// dt/dz, with the row's sum s.  Where g is positive, g / s goes into the
-// exponent c: the result is off by 2^-24 of that exponent, far below its
-// rounding to bf16.
+// dt/dz, with the row's sum s.  Where g is positive and c = log2(g / s) - |k| m
+// is below kDsFast, g / s goes into the exponent: c's rounding (2^-25 of it, at
+// most 2^-17) and that of the logarithms put the result off by 10^-5 of its
+// value, a four-hundredth of its rounding to bf16.
+constexpr float kDsFast = 256.0f;
 template <bool CAP>
 __device__ __forceinline__ uint4 ds_grad8(const DsArgs& a, const uint4& v, float c) {
     float x[8];
@@ -346,15 +362,29 @@ __device__ __forceinline__ uint4 ds_grad8(const DsArgs& a, const uint4& v, float
     }
     return round8(x);
 }
-// The same for any g and m.
+// The same for any g and m: exponents as the row's sum has them (ds_power; m0 =
+// -0 or c = 0 drop out), then log2(|g| / s) is added, so that probabilities far
+// below the row's largest are not lost between the reference and the sum.
 template <bool CAP>
-__device__ __noinline__ uint4 ds_grad8_any(const DsArgs& a, const uint4 v, float m, float inv_s, float g) {
+__device__ __noinline__ uint4 ds_grad8_any(const DsArgs& a, const uint4 v, float m, float log_s, float g) {
     float x[8];
     ds_args8<CAP>(a, v, x);
+    const bool far = ds_far(a, m);
+    const float m0 = far ? -ds_origin<CAP>(a, m) : -0.0f, c = far ? 0.0f : -ds_exponent(a, m);
+    const float l = log2f(fabsf(g)) - log_s, sign = copysignf(1.0f, g);
+    const uint64_t kk = f2_packf(a.k, a.k), mm = f2_packf(m0, m0), cc = f2_packf(c, c);
+    const uint64_t ll = f2_packf(l, l), ss = f2_packf(sign, sign);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float y = ds_rel<CAP>(a, x[e], m) * inv_s * g;
-        x[e] = CAP ? y * fmaf(-x[e], x[e], -x[e]) : y;
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t x2 = f2_packf(x[2 * i], x[2 * i + 1]);
+        float lo, hi;
+        f2_unpack(f2_add(f2_fma(f2_add(x2, mm), kk, cc), ll), lo, hi);
+        uint64_t y2 = f2_mul(f2_packf(ds_ex2(lo), ds_ex2(hi)), ss);
+        if (CAP) {
+            const uint64_t n2 = f2_packf(-x[2 * i], -x[2 * i + 1]);
+            y2 = f2_mul(y2, f2_fma(x2, n2, n2));
+        }
+        f2_unpack(y2, x[2 * i], x[2 * i + 1]);
     }
     return round8(x);
 }
@@ -448,8 +478,8 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
         if (a.factor != nullptr) g *= a.factor[1];
         return g;
     };
-    const auto element = [&](float z, float p, float m, float s, float g) {
-        const float d = (ds_rel<CAP>(a, z, m) / s - p) * g;
+    const auto element = [&](float z, float p, float m, float log_s, float g) {
+        const float d = (ds_ex2(ds_power<CAP>(a, z, m) - log_s) - p) * g;
         return __float2bfloat16(CAP ? 4.0f * d * fmaf(-z, z, -z) : d);
     };
     if (!teaches) {
@@ -498,9 +528,9 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
         ds_cluster_wait();  // every block's shared memory can be stored to
         float m = CAP ? -0.5f : 0.0f;  // the reference of sums
         uint32_t again = 0u;           // exchanges for rows summed again
-        float sm = m, c = 0.0f;        // that of the row being summed, and - its exponent
+        float c = 0.0f;                // - the exponent of the one that the row being summed has
         uint64_t acc = 0u;
-        float om = 0.0f, os = 0.0f, og = 0.0f, oc = 0.0f;  // of the row being turned into gradient
+        float om = 0.0f, os = 0.0f, olog = 0.0f, og = 0.0f, oc = 0.0f;  // of the row being turned into gradient
         bool live = false, fast = false, skip = false;
         float up = 0.0f, dloss = a.dloss != nullptr ? a.dloss[first * a.dloss_stride] : 1.0f;  // factors of the upstream gradient
         const int steps = rows * a.chunks;
@@ -509,7 +539,6 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
             if (k < steps) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kDsAhead - 1) : "memory");
                 if (sum_c == 0) {
-                    sm = m;
                     c = -ds_exponent(a, m);
                     acc = 0u;
                     skip = skips >> (ask_i - sum_i) & 1u;
@@ -531,7 +560,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                     // V need not be a multiple of 8, nor the row padded: the
                     // logits behind the last whole vector go to one thread each
                     if (!skip && tid < ntail)
-                        lo += ds_rel<CAP>(a, ds_arg<CAP>(a, __bfloat162float(sum_z[8 * nfull + tid])), sm);
+                        lo += ds_ex2(fmaf(ds_arg<CAP>(a, __bfloat162float(sum_z[8 * nfull + tid])), a.k, c));
                     // (an ignored row's is 1, so that nobody sums it again)
                     ds_send(sums + (sum_i % kDsDepth) * cells, rank * W + warp, cluster,
                             static_cast<uint32_t>(sum_i) + 1u, skip ? 1.0f : ds_warp_sum(lo));
@@ -563,7 +592,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                         cell = sums_again + (again++ & 1u) * cells;
                         ds_send(cell, rank * W + warp, cluster, again, ds_warp_sum(ds_slice_sum<CAP, T>(a, z, n, om)));
                         if (!ds_receive<false>(a, sh, cell, cells, again, os)) break;
-                        m = om;
+                        if (!ds_far(a, om)) m = om;  // the first pass forms no differences
                     }
                     if (tid == 0) {
                         *static_cast<volatile float*>(&sh.told[buf][0]) = om;
@@ -579,8 +608,9 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                         og = up * dloss;
                         // asked for now, used at the next row
                         dloss = a.dloss != nullptr && i + 1 < rows ? a.dloss[(out_row + stride) * a.dloss_stride] : 1.0f;
-                        oc = log2f(og) - log2f(os) + (CAP ? 2.0f : 0.0f) - ds_exponent(a, om);
-                        fast = live && !ds_far<CAP>(a, om) && og > 0.0f;
+                        olog = log2f(os);
+                        oc = log2f(og) - olog + (CAP ? 2.0f : 0.0f) - ds_exponent(a, om);
+                        fast = live && og > 0.0f && fabsf(oc) < kDsFast && !ds_far(a, om);
                         out_z = reinterpret_cast<uint4*>(a.dz + out_row * a.ld + c0) + tid;
                     }
                 }
@@ -593,7 +623,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                     } else {
 #pragma unroll 1
                         for (int b = 0; tid + b * T < len; ++b)
-                            __stcs(out_z + b * T, live ? ds_grad8_any<CAP>(a, out_at[b * T], om, 1.0f / os, CAP ? 4.0f * og : og)
+                            __stcs(out_z + b * T, live ? ds_grad8_any<CAP>(a, out_at[b * T], om, olog, CAP ? 4.0f * og : og)
                                                        : make_uint4(0u, 0u, 0u, 0u));
                     }
                     out_z += chunk;
@@ -603,7 +633,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                     if (GRAD) {
                         if (tid < ntail) {
                             const long long at = out_row * a.ld + c0 + 8 * nfull + tid;
-                            a.dz[at] = live ? element(ds_arg<CAP>(a, __bfloat162float(a.z[at])), 0.0f, om, os, og)
+                            a.dz[at] = live ? element(ds_arg<CAP>(a, __bfloat162float(a.z[at])), 0.0f, om, olog, og)
                                             : __float2bfloat16(0.0f);
                         }
                         __syncwarp();
@@ -644,14 +674,13 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
             const float m = ds_look(&sh.told[buf][0]), s = ds_look(&sh.told[buf][1]);
             wait_prior();
             if (wants_loss) {
-                const bool far = ds_far<CAP>(a, m);
                 const float log_s = logf(s);
                 constexpr float kLn2 = 0.6931471805599453f;
                 float sum = 0.0f;
                 for (int e = lane; t.live && e < a.K; e += 32) {
                     const float p = t.tp[e] * t.inv_psum;
                     if (p == 0.0f || t.tc[e] < 0) continue;
-                    const float y = far ? (t.tx[e] - a.sign * m) * a.k : fmaf(t.tx[e], a.k, -ds_exponent(a, m));
+                    const float y = ds_power<CAP>(a, t.tx[e], m);
                     sum += p * ((t.tl[e] - t.log_psum) - (y * kLn2 - log_s));
                 }
                 sum = ds_warp_sum(sum);
@@ -659,7 +688,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
             }
             if (t.bad && rank == 0 && lane == 0) atomicExch(a.status, kStatusBad);
             if (GRAD) {
-                const float g = upstream(row);
+                const float g = upstream(row), log_s = log2f(s);
                 const uint32_t done = ds_smem(&sh.done[warp - W]), parity = static_cast<uint32_t>(i / kDsTeachers) & 1u;
                 if (!ds_wait(a, sh, [&] { return mbar_try_wait(done, parity); })) break;
                 __nv_bfloat16* dz = a.dz + row * a.ld;
@@ -677,7 +706,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                         }
                         if (before) continue;
                     }
-                    dz[c] = element(t.tx[e], p * t.inv_psum, m, s, g);
+                    dz[c] = element(t.tx[e], p * t.inv_psum, m, log_s, g);
                 }
                 __syncwarp();
             }
