@@ -34,9 +34,9 @@
 // from the reference, which is fp32's own precision of it.
 //
 // With softcapping, t = cap tanh(s z / cap)
-// = cap - 2 cap r with r = 1 / (1 + 2^(cap2 z)): exponents are taken of -r,
-// dt/dz = 4 s r (1 - r) has no cancellation where tanh saturates, and four
-// logits share one reciprocal.
+// = cap - 2 cap r with r = 1 / (1 + e), e = 2^(cap2 z): exponents are taken of
+// -r, dt/dz = 4 s e r^2 has no cancellation where tanh saturates on either side,
+// and four logits share one reciprocal.
 //
 // On a B200: 4096 rows of 128256 logits, loss and gradient, 454 us (4.6 TB/s; the
 // same stream of chunks merely copied takes 390, the exponentials' unit 248); the
@@ -113,31 +113,66 @@ __device__ __forceinline__ void ds_cluster_arrive() { asm volatile("barrier.clus
 __device__ __forceinline__ void ds_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // What exponents are taken of: z, or -r (see above).  2^(cap2 z) is held to
-// 2^30, where tanh is 1 in fp32 already, so that a product of four
-// denominators stays in range; min keeps a NaN.
-__device__ __forceinline__ float ds_denominator(const DsArgs& a, float z) {
+// 2^30, where tanh is 1 in fp32 already (and dt/dz below 2^-28 s), so that a
+// product of four denominators stays in range; min keeps a NaN.
+__device__ __forceinline__ float ds_cap_exp(float power) {
     float e;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(e) : "f"(a.cap2 * z), "f"(30.0f));
-    return 1.0f + ds_ex2(e);
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(e) : "f"(power), "f"(30.0f));
+    return ds_ex2(e);
 }
 template <bool CAP>
 __device__ __forceinline__ float ds_arg(const DsArgs& a, float z) {
-    return CAP ? -ds_rcp(ds_denominator(a, z)) : z;
+    return CAP ? -ds_rcp(1.0f + ds_cap_exp(a.cap2 * z)) : z;
+}
+// The same of single logits, and dt/dz / s, by CUDA's own functions.
+template <bool CAP>
+__device__ __forceinline__ float ds_arg_one(const DsArgs& a, float z) {
+    return CAP ? -1.0f / (1.0f + expf(2.0f * (a.scale / a.cap * z))) : z;
 }
 template <bool CAP>
-__device__ __forceinline__ void ds_args8(const DsArgs& a, const uint4& v, float (&x)[8]) {
-    widen8(v, x);
-    if constexpr (CAP) {
+__device__ __forceinline__ float ds_slope_one(const DsArgs& a, float z) {
+    if (!CAP) return 1.0f;
+    const float e = expf(-2.0f * fabsf(a.scale / a.cap * z));
+    return 4.0f * e / ((1.0f + e) * (1.0f + e));
+}
+// Of eight, as packed fp32 pairs: neighbours, or with softcapping elements
+// (0, 2), (1, 3), (4, 6), (5, 7), and e of each.
+__device__ __forceinline__ uint64_t ds_pair(float v) { return f2_packf(v, v); }
+template <bool CAP>
+__device__ __forceinline__ void ds_args8(const DsArgs& a, const uint4& v, uint64_t (&x)[4], uint64_t (&e)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int h = 0; h < 8; h += 4) {
-            float d[4];
+    for (int h = 0; h < 4; h += 2) {
+        if constexpr (!CAP) {
+            x[h] = f2_pack(w[h] << 16, w[h] & 0xFFFF0000u);
+            x[h + 1] = f2_pack(w[h + 1] << 16, w[h + 1] & 0xFFFF0000u);
+        } else {
+            x[h] = f2_pack(w[h] << 16, w[h + 1] << 16);
+            x[h + 1] = f2_pack(w[h] & 0xFFFF0000u, w[h + 1] & 0xFFFF0000u);
+            uint64_t d[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = ds_denominator(a, x[h + i]);
-            const float d01 = d[0] * d[1], d23 = d[2] * d[3], r = ds_rcp(d01 * d23);
-            const float n01 = -r * d23, n23 = -r * d01;
-            x[h] = n01 * d[1], x[h + 1] = n01 * d[0], x[h + 2] = n23 * d[3], x[h + 3] = n23 * d[2];
+            for (int i = 0; i < 2; ++i) {
+                float lo, hi;
+                f2_unpack(f2_mul(x[h + i], ds_pair(a.cap2)), lo, hi);
+                e[h + i] = f2_packf(ds_cap_exp(lo), ds_cap_exp(hi));
+                d[i] = f2_add(e[h + i], ds_pair(1.0f));
+            }
+            float d01, d23;
+            f2_unpack(f2_mul(d[0], d[1]), d01, d23);
+            const uint64_t n = f2_mul(ds_pair(-ds_rcp(d01 * d23)), f2_packf(d23, d01));
+            x[h] = f2_mul(n, d[1]), x[h + 1] = f2_mul(n, d[0]);
         }
     }
+}
+template <bool CAP>
+__device__ __forceinline__ uint4 ds_round8(const uint64_t (&x)[4]) {
+    float f[8];
+#pragma unroll
+    for (int h = 0; h < 4; h += 2) {
+        f2_unpack(x[h], f[2 * h], f[2 * h + (CAP ? 2 : 1)]);
+        f2_unpack(x[h + 1], f[2 * h + (CAP ? 1 : 2)], f[2 * h + 3]);
+    }
+    return round8(f);
 }
 
 __device__ __forceinline__ float ds_warp_max(float v) {
@@ -262,9 +297,8 @@ __device__ __forceinline__ bool ds_receive(const DsArgs& a, DsShared& sh, const 
 }
 
 // The teacher's entries of a row, in one warp's hands: ids to tc, exp((a -
-// max) / T) to tp, its exponent to tl, and to tx what the student's exponents
-// are taken of at the ids of this block's slice, for the loss (`all`) at every
-// id.
+// max) / T) to tp, its exponent to tl, and to tx the student's logits at the ids
+// of this block's slice, for the loss (`all`) at every id.
 struct DsTeacher {
     float *tp, *tl, *tx;
     int *tc, *table;
@@ -272,7 +306,6 @@ struct DsTeacher {
     bool bad, live, twice;  // twice: an id stands more than once
 };
 
-template <bool CAP>
 __device__ __forceinline__ void ds_teacher(const DsArgs& a, DsTeacher& t, long long row, long long c0, int n, bool all) {
     const int lane = threadIdx.x & 31, places = 1 << a.log_table;
     for (int i = lane; i < places; i += 32) t.table[i] = -1;
@@ -292,10 +325,7 @@ __device__ __forceinline__ void ds_teacher(const DsArgs& a, DsTeacher& t, long l
         if (in) {
             amax = fmaxf(amax, v);
             any = any || !(v == -INFINITY);
-            if (all || (id >= c0 && id < c0 + n)) {
-                const float z = __bfloat162float(a.z[row * a.ld + id]);
-                t.tx[i] = CAP ? -1.0f / (1.0f + expf(2.0f * (a.scale / a.cap * z))) : z;
-            }
+            if (all || (id >= c0 && id < c0 + n)) t.tx[i] = __bfloat162float(a.z[row * a.ld + id]);
             // at most K ids for at least 2 K places: a free one is found
             const int c = static_cast<int>(id);
             int at_table = static_cast<int>((static_cast<uint32_t>(c) * 2654435769u) >> (32 - a.log_table));
@@ -325,13 +355,13 @@ __device__ __forceinline__ void ds_teacher(const DsArgs& a, DsTeacher& t, long l
 }
 
 // 2^(x k + c) of eight, added to acc two by two.
-__device__ __forceinline__ void ds_add8(const DsArgs& a, const float (&x)[8], float c, uint64_t& acc) {
-    const uint64_t kk = f2_packf(a.k, a.k), cc = f2_packf(c, c);
+__device__ __forceinline__ void ds_add8(const DsArgs& a, const uint64_t (&x)[4], float c, uint64_t& acc) {
+    const uint64_t kk = ds_pair(a.k), cc = ds_pair(c);
     uint64_t e[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float lo, hi;
-        f2_unpack(f2_fma(f2_packf(x[2 * i], x[2 * i + 1]), kk, cc), lo, hi);
+        f2_unpack(f2_fma(x[i], kk, cc), lo, hi);
         e[i] = f2_packf(ds_ex2(lo), ds_ex2(hi));
     }
     acc = f2_add(acc, f2_add(f2_add(e[0], e[1]), f2_add(e[2], e[3])));
@@ -345,48 +375,40 @@ __device__ __forceinline__ void ds_add8(const DsArgs& a, const float (&x)[8], fl
 constexpr float kDsFast = 256.0f;
 template <bool CAP>
 __device__ __forceinline__ uint4 ds_grad8(const DsArgs& a, const uint4& v, float c) {
-    float x[8];
-    ds_args8<CAP>(a, v, x);
-    const uint64_t kk = f2_packf(a.k, a.k), cc = f2_packf(c, c);
+    uint64_t x[4], e[4];
+    ds_args8<CAP>(a, v, x, e);
+    const uint64_t kk = ds_pair(a.k), cc = ds_pair(c);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint64_t x2 = f2_packf(x[2 * i], x[2 * i + 1]);
         float lo, hi;
-        f2_unpack(f2_fma(x2, kk, cc), lo, hi);
-        uint64_t y2 = f2_packf(ds_ex2(lo), ds_ex2(hi));
-        if (CAP) {  // r (1 - r) = -x^2 - x
-            const uint64_t n2 = f2_packf(-x[2 * i], -x[2 * i + 1]);
-            y2 = f2_mul(y2, f2_fma(x2, n2, n2));
-        }
-        f2_unpack(y2, x[2 * i], x[2 * i + 1]);
+        f2_unpack(f2_fma(x[i], kk, cc), lo, hi);
+        uint64_t y = f2_packf(ds_ex2(lo), ds_ex2(hi));
+        if (CAP) y = f2_mul(y, f2_mul(e[i], f2_mul(x[i], x[i])));
+        x[i] = y;
     }
-    return round8(x);
+    return ds_round8<CAP>(x);
 }
 // The same for any g and m: exponents as the row's sum has them (ds_power; m0 =
 // -0 or c = 0 drop out), then log2(|g| / s) is added, so that probabilities far
 // below the row's largest are not lost between the reference and the sum.
 template <bool CAP>
 __device__ __noinline__ uint4 ds_grad8_any(const DsArgs& a, const uint4 v, float m, float log_s, float g) {
-    float x[8];
-    ds_args8<CAP>(a, v, x);
+    uint64_t x[4], e[4];
+    ds_args8<CAP>(a, v, x, e);
     const bool far = ds_far(a, m);
     const float m0 = far ? -ds_origin<CAP>(a, m) : -0.0f, c = far ? 0.0f : -ds_exponent(a, m);
-    const float l = log2f(fabsf(g)) - log_s, sign = copysignf(1.0f, g);
-    const uint64_t kk = f2_packf(a.k, a.k), mm = f2_packf(m0, m0), cc = f2_packf(c, c);
-    const uint64_t ll = f2_packf(l, l), ss = f2_packf(sign, sign);
+    const float l = log2f(fabsf(g)) - log_s;
+    const uint64_t kk = ds_pair(a.k), mm = ds_pair(m0), cc = ds_pair(c), ll = ds_pair(l);
+    const uint64_t sign = ds_pair(copysignf(1.0f, g));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint64_t x2 = f2_packf(x[2 * i], x[2 * i + 1]);
         float lo, hi;
-        f2_unpack(f2_add(f2_fma(f2_add(x2, mm), kk, cc), ll), lo, hi);
-        uint64_t y2 = f2_mul(f2_packf(ds_ex2(lo), ds_ex2(hi)), ss);
-        if (CAP) {
-            const uint64_t n2 = f2_packf(-x[2 * i], -x[2 * i + 1]);
-            y2 = f2_mul(y2, f2_fma(x2, n2, n2));
-        }
-        f2_unpack(y2, x[2 * i], x[2 * i + 1]);
+        f2_unpack(f2_add(f2_fma(f2_add(x[i], mm), kk, cc), ll), lo, hi);
+        uint64_t y = f2_mul(f2_packf(ds_ex2(lo), ds_ex2(hi)), sign);
+        if (CAP) y = f2_mul(y, f2_mul(e[i], f2_mul(x[i], x[i])));
+        x[i] = y;
     }
-    return round8(x);
+    return ds_round8<CAP>(x);
 }
 
 // This thread's largest sign * z (-r) of a slice in global memory, and its sum
@@ -479,8 +501,8 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
         return g;
     };
     const auto element = [&](float z, float p, float m, float log_s, float g) {
-        const float d = (ds_ex2(ds_power<CAP>(a, z, m) - log_s) - p) * g;
-        return __float2bfloat16(CAP ? 4.0f * d * fmaf(-z, z, -z) : d);
+        const float q = ds_ex2(ds_power<CAP>(a, ds_arg_one<CAP>(a, z), m) - log_s);
+        return __float2bfloat16((q - p) * g * ds_slope_one<CAP>(a, z));
     };
     if (!teaches) {
         // Three places in the stream: where chunks are asked for, summed, and
@@ -548,8 +570,8 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
 #pragma unroll
                 for (int b = 0; b < B; ++b)
                     if (tid + b * T < len) {
-                        float z[8];
-                        ds_args8<CAP>(a, sum_at[b * T], z);
+                        uint64_t z[4], e[4];
+                        ds_args8<CAP>(a, sum_at[b * T], z, e);
                         ds_add8(a, z, c, acc);
                     }
                 step(sum_at);
@@ -633,7 +655,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                     if (GRAD) {
                         if (tid < ntail) {
                             const long long at = out_row * a.ld + c0 + 8 * nfull + tid;
-                            a.dz[at] = live ? element(ds_arg<CAP>(a, __bfloat162float(a.z[at])), 0.0f, om, olog, og)
+                            a.dz[at] = live ? element(__bfloat162float(a.z[at]), 0.0f, om, olog, og)
                                             : __float2bfloat16(0.0f);
                         }
                         __syncwarp();
@@ -659,7 +681,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
             const long long row = first + static_cast<long long>(i) * stride;
             const int buf = i % kDsDepth;
             t.live = t.bad = false;
-            if (!ignored(row)) ds_teacher<CAP>(a, t, row, c0, n, wants_loss);
+            if (!ignored(row)) ds_teacher(a, t, row, c0, n, wants_loss);
             __threadfence_block();  // what was read of the logits has arrived: it is in tx
             __syncwarp();
             if (lane == 0) *static_cast<volatile int*>(&sh.ready[buf]) = (i + 1) * 2 + t.live;
@@ -680,7 +702,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                 for (int e = lane; t.live && e < a.K; e += 32) {
                     const float p = t.tp[e] * t.inv_psum;
                     if (p == 0.0f || t.tc[e] < 0) continue;
-                    const float y = ds_power<CAP>(a, t.tx[e], m);
+                    const float y = ds_power<CAP>(a, ds_arg_one<CAP>(a, t.tx[e]), m);
                     sum += p * ((t.tl[e] - t.log_psum) - (y * kLn2 - log_s));
                 }
                 sum = ds_warp_sum(sum);

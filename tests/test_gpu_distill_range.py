@@ -122,3 +122,28 @@ def test_all_of_a_cluster_at_a_masks_value():
     run_and_check(z, values, ids, np.full(N, 0.5, dtype=np.float32))
     dz = api.distill_backward(padded(z)[0], values.cuda(), ids.cuda(), torch.full((N,), 0.5, device="cuda"))
     assert float(dz.float().max()) <= 0.5 / V * (1 + 2.0 ** -7)
+
+
+@pytest.mark.parametrize("N,V", SIZES)
+@pytest.mark.parametrize("s,T", [(1.0, 1.0), (-0.5, 2.0)])
+def test_softcap_slope_far_from_zero(N, V, s, T):
+    """dt/dz where tanh is near -1 or 1, down to 10^-8, at the teacher's entries and others.
+
+    Tolerance, relative to the slope itself: 2^-8 of the result for its rounding, 2^-17 for the slope's (an exponent of
+    at most 30 off by 2^-23 of it, 2.5e-6, twice), and the probabilities' d of test_gpu_distill.py."""
+    rng = np.random.default_rng(V + 4)
+    cap = 30.0
+    z, values, ids = make(rng, N, V, 6, 10.0, abs(s))
+    z[::2] = torch.from_numpy(rng.uniform(-300.0, 300.0, z[::2].shape)).to(z.dtype) / abs(s)
+    dev, _ = padded(z)
+    dloss = rng.uniform(0.5, 1.5, N).astype(np.float32)
+    kw = dict(temperature=T, logit_scale=s, softcap=cap)
+    dz = f64(api.distill_backward(dev, values.cuda(), ids.cuda(), torch.from_numpy(dloss).cuda(), **kw))
+    z64 = f64(z)
+    rl, rd, q, P = ods.run(z64, f64(values), ids.numpy().astype(np.int64), dloss, None, T, s, cap)
+    x = cap * np.tanh(s * z64 / cap) / T
+    d = 2e-5 + 2.0 ** -21 * (x.max(axis=1, keepdims=True) - x) + 2.0 ** -19 * cap / T
+    slope = abs(s) / np.cosh(s * z64 / cap) ** 2
+    tol = (2.0 ** -8 + 2.0 ** -17) * np.abs(rd) + (T * dloss)[:, None] * slope * (q + P) * d + 2.0 ** -126
+    bad = ~(np.abs(dz - rd) <= tol)
+    assert not np.any(bad), (np.argwhere(bad)[:4], dz[bad][:4], rd[bad][:4], tol[bad][:4])
