@@ -34,6 +34,12 @@
  * The quotients 1 / T and s / T (with softcapping cap / T and s / cap) must stay
  * below 10^37.
  *
+ * Logarithms of probabilities are fp32's: off by some 10^-5 and 2^-21 of their
+ * distance from the row's largest, whatever the level of the logits.  With
+ * softcapping 2^-22 cap / T is added up to cap = 128 T; above, t is formed to
+ * fp32's precision first (2^-20 of the row's largest |t| / T), which takes about
+ * 1.8 times as long.  Probabilities and gradients below 2^-126 may be 0.
+ *
  * A teacher id below -1 or not below V is a device-side finding: the entry
  * counts as absent, the row's loss is NaN, and lora_step_device_status reports
  * LORA_MLP_ERR_INVALID_ARG.  LORA_MLP_ERR_DEVICE_TIMEOUT there means that a

@@ -36,7 +36,11 @@
 // With softcapping, t = cap tanh(s z / cap)
 // = cap - 2 cap r with r = 1 / (1 + e), e = 2^(cap2 z): exponents are taken of
 // -r, dt/dz = 4 s e r^2 has no cancellation where tanh saturates on either side,
-// and four logits share one reciprocal.
+// and four logits share one reciprocal.  t / T is off by 2^-22 cap / T so,
+// however small t is: fp32 holds r, near 1/2, to 2^-24.  That is a choice for
+// speed up to cap / T = 128 (3e-5; 1024 rows of 256000 take 415 us so, 746 us
+// with tanhf).  Above it t itself is what exponents are taken of, to fp32's
+// precision of t, and rows are else treated as without softcapping.
 //
 // On a B200: 4096 rows of 128256 logits, loss and gradient, 454 us (4.6 TB/s; the
 // same stream of chunks merely copied takes 390, the exponentials' unit 248); the
@@ -59,6 +63,9 @@ constexpr int kDsDepth = 8;     // rows under way (see DsShared)
 constexpr int kDsTeachers = 3;  // warps that take the teacher's part, a row each in turn
 constexpr int kDsTimeout = -7;  // LORA_MLP_ERR_DEVICE_TIMEOUT
 constexpr int kDsEntryBytes = 16;  // of shared memory for a teacher's entry, and 4 for each place of the table of ids
+// How exponents are formed: of z, of -r, of t (the kernel's parameter CAP).
+constexpr int kDsNoCap = 0, kDsCap = 1, kDsWideCap = 2;
+constexpr float kDsWide = 128.0f;  // cap / T above which t is formed
 constexpr float kDsLowest = -3.3895313892515355e38f;  // bf16's lowest finite value
 
 struct DsArgs {
@@ -79,9 +86,11 @@ struct DsArgs {
     long long ignore;
     float inv_T, T;
     float scale, cap;     // s, cap or 0
+    int form;             // kDsNoCap, kDsCap, kDsWideCap (the host's; the kernel has it as a parameter)
     float sign;           // of s: the largest exponent is that of the largest sign * z
-    float k;              // base-2 exponent of a unit of z: s log2(e) / T; of a unit of -r: 2 cap log2(e) / T
+    float k;              // base-2 exponent of a unit of z: s log2(e) / T; of -r: 2 cap log2(e) / T; of t: log2(e) / T
     float cap2;           // 2 s / cap * log2(e)
+    float ratio, ratio2;  // their product is s / cap: two, as it may be below fp32's normal numbers
     float* loss;          // may be null
     float* out;           // the reduced loss, or null
     uint32_t* counter;    // clusters done, zero before the launch (with out)
@@ -112,7 +121,7 @@ __device__ __forceinline__ uint32_t ds_rank() {
 __device__ __forceinline__ void ds_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void ds_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// What exponents are taken of: z, or -r (see above).  2^(cap2 z) is held to
+// What exponents are taken of: z, -r or t (see above).  2^(cap2 z) is held to
 // 2^30, where tanh is 1 in fp32 already (and dt/dz below 2^-28 s), so that a
 // product of four denominators stays in range; min keeps a NaN.
 __device__ __forceinline__ float ds_cap_exp(float power) {
@@ -120,32 +129,51 @@ __device__ __forceinline__ float ds_cap_exp(float power) {
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(e) : "f"(power), "f"(30.0f));
     return ds_ex2(e);
 }
-template <bool CAP>
+// s z / cap, t and dt/dz / s = 1 / cosh^2(s z / cap).
+__device__ __forceinline__ float ds_wide_arg(const DsArgs& a, float z) { return z * a.ratio * a.ratio2; }
+__device__ __forceinline__ float ds_wide(const DsArgs& a, float u) { return a.cap * tanhf(u); }
+__device__ __forceinline__ float ds_wide_slope(float u) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float e = ds_ex2(-2.0f * kLog2e * fabsf(u)), r = ds_rcp(1.0f + e);
+    return 4.0f * e * r * r;
+}
+template <int CAP>
 __device__ __forceinline__ float ds_arg(const DsArgs& a, float z) {
+    if (CAP == kDsWideCap) return ds_wide(a, ds_wide_arg(a, z));
     return CAP ? -ds_rcp(1.0f + ds_cap_exp(a.cap2 * z)) : z;
 }
 // The same of single logits, and dt/dz / s, by CUDA's own functions.
-template <bool CAP>
+template <int CAP>
 __device__ __forceinline__ float ds_arg_one(const DsArgs& a, float z) {
-    return CAP ? -1.0f / (1.0f + expf(2.0f * (a.scale / a.cap * z))) : z;
+    return CAP == kDsCap ? -1.0f / (1.0f + expf(2.0f * ds_wide_arg(a, z))) : ds_arg<CAP>(a, z);
 }
-template <bool CAP>
+template <int CAP>
 __device__ __forceinline__ float ds_slope_one(const DsArgs& a, float z) {
     if (!CAP) return 1.0f;
-    const float e = expf(-2.0f * fabsf(a.scale / a.cap * z));
+    const float e = expf(-2.0f * fabsf(ds_wide_arg(a, z)));
     return 4.0f * e / ((1.0f + e) * (1.0f + e));
 }
-// Of eight, as packed fp32 pairs: neighbours, or with softcapping elements
-// (0, 2), (1, 3), (4, 6), (5, 7), and e of each.
+// Of eight, as packed fp32 pairs: neighbours, or of -r elements (0, 2), (1, 3),
+// (4, 6), (5, 7); and what dt/dz takes of each, e of -r, the slope of t.
 __device__ __forceinline__ uint64_t ds_pair(float v) { return f2_packf(v, v); }
-template <bool CAP>
+template <int CAP>
 __device__ __forceinline__ void ds_args8(const DsArgs& a, const uint4& v, uint64_t (&x)[4], uint64_t (&e)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int h = 0; h < 4; h += 2) {
-        if constexpr (!CAP) {
+        if constexpr (CAP != kDsCap) {
             x[h] = f2_pack(w[h] << 16, w[h] & 0xFFFF0000u);
             x[h + 1] = f2_pack(w[h + 1] << 16, w[h + 1] & 0xFFFF0000u);
+            if constexpr (CAP == kDsWideCap) {
+#pragma unroll
+                for (int i = h; i < h + 2; ++i) {
+                    float lo, hi;
+                    f2_unpack(x[i], lo, hi);
+                    lo = ds_wide_arg(a, lo), hi = ds_wide_arg(a, hi);
+                    x[i] = f2_packf(ds_wide(a, lo), ds_wide(a, hi));
+                    e[i] = f2_packf(ds_wide_slope(lo), ds_wide_slope(hi));
+                }
+            }
         } else {
             x[h] = f2_pack(w[h] << 16, w[h + 1] << 16);
             x[h + 1] = f2_pack(w[h] & 0xFFFF0000u, w[h + 1] & 0xFFFF0000u);
@@ -164,13 +192,13 @@ __device__ __forceinline__ void ds_args8(const DsArgs& a, const uint4& v, uint64
         }
     }
 }
-template <bool CAP>
+template <int CAP>
 __device__ __forceinline__ uint4 ds_round8(const uint64_t (&x)[4]) {
     float f[8];
 #pragma unroll
     for (int h = 0; h < 4; h += 2) {
-        f2_unpack(x[h], f[2 * h], f[2 * h + (CAP ? 2 : 1)]);
-        f2_unpack(x[h + 1], f[2 * h + (CAP ? 1 : 2)], f[2 * h + 3]);
+        f2_unpack(x[h], f[2 * h], f[2 * h + (CAP == kDsCap ? 2 : 1)]);
+        f2_unpack(x[h + 1], f[2 * h + (CAP == kDsCap ? 1 : 2)], f[2 * h + 3]);
     }
     return round8(f);
 }
@@ -186,7 +214,7 @@ __device__ __forceinline__ float ds_warp_sum(float v) {
     return v;
 }
 
-// References m are kept as sign * z (as -r with softcapping), so that more is
+// References m are kept as sign * z (as -r or t with softcapping), so that more is
 // more whatever the sign of k; |k| m is their exponent.
 __device__ __forceinline__ float ds_exponent(const DsArgs& a, float m) { return __fmul_rn(m, fabsf(a.k)); }
 // Whether it is so large that its rounding alone (2^-24 of it) shifts the sums
@@ -195,16 +223,16 @@ __device__ __forceinline__ float ds_exponent(const DsArgs& a, float m) { return 
 constexpr float kDsFar = 0x1p20f;
 __device__ __forceinline__ bool ds_far(const DsArgs& a, float m) { return !(fabsf(ds_exponent(a, m)) < kDsFar); }
 // m as what exponents are taken of.
-template <bool CAP>
+template <int CAP>
 __device__ __forceinline__ float ds_origin(const DsArgs& a, float m) {
     return CAP ? m : a.sign * m;
 }
 // The exponent of a term of a sum that is relative to m.
-template <bool CAP>
+template <int CAP>
 __device__ __forceinline__ float ds_power(const DsArgs& a, float x, float m) {
     return ds_far(a, m) ? (x - ds_origin<CAP>(a, m)) * a.k : fmaf(x, a.k, -ds_exponent(a, m));
 }
-template <bool CAP>
+template <int CAP>
 __device__ __forceinline__ float ds_rel(const DsArgs& a, float x, float m) {
     return ds_ex2(ds_power<CAP>(a, x, m));
 }
@@ -373,7 +401,7 @@ __device__ __forceinline__ void ds_add8(const DsArgs& a, const uint64_t (&x)[4],
 // most 2^-17) and that of the logarithms put the result off by 10^-5 of its
 // value, a four-hundredth of its rounding to bf16.
 constexpr float kDsFast = 256.0f;
-template <bool CAP>
+template <int CAP>
 __device__ __forceinline__ uint4 ds_grad8(const DsArgs& a, const uint4& v, float c) {
     uint64_t x[4], e[4];
     ds_args8<CAP>(a, v, x, e);
@@ -383,7 +411,7 @@ __device__ __forceinline__ uint4 ds_grad8(const DsArgs& a, const uint4& v, float
         float lo, hi;
         f2_unpack(f2_fma(x[i], kk, cc), lo, hi);
         uint64_t y = f2_packf(ds_ex2(lo), ds_ex2(hi));
-        if (CAP) y = f2_mul(y, f2_mul(e[i], f2_mul(x[i], x[i])));
+        if (CAP) y = f2_mul(y, CAP == kDsCap ? f2_mul(e[i], f2_mul(x[i], x[i])) : e[i]);
         x[i] = y;
     }
     return ds_round8<CAP>(x);
@@ -391,7 +419,7 @@ __device__ __forceinline__ uint4 ds_grad8(const DsArgs& a, const uint4& v, float
 // The same for any g and m: exponents as the row's sum has them (ds_power; m0 =
 // -0 or c = 0 drop out), then log2(|g| / s) is added, so that probabilities far
 // below the row's largest are not lost between the reference and the sum.
-template <bool CAP>
+template <int CAP>
 __device__ __noinline__ uint4 ds_grad8_any(const DsArgs& a, const uint4 v, float m, float log_s, float g) {
     uint64_t x[4], e[4];
     ds_args8<CAP>(a, v, x, e);
@@ -405,21 +433,24 @@ __device__ __noinline__ uint4 ds_grad8_any(const DsArgs& a, const uint4 v, float
         float lo, hi;
         f2_unpack(f2_add(f2_fma(f2_add(x[i], mm), kk, cc), ll), lo, hi);
         uint64_t y = f2_mul(f2_packf(ds_ex2(lo), ds_ex2(hi)), sign);
-        if (CAP) y = f2_mul(y, f2_mul(e[i], f2_mul(x[i], x[i])));
+        if (CAP) y = f2_mul(y, CAP == kDsCap ? f2_mul(e[i], f2_mul(x[i], x[i])) : e[i]);
         x[i] = y;
     }
     return ds_round8<CAP>(x);
 }
 
-// This thread's largest sign * z (-r) of a slice in global memory, and its sum
+// This thread's largest sign * z (-r, t) of a slice in global memory, and its sum
 // relative to m: for rows whose sum came out too large or too small.
-template <bool CAP, int T>
+template <int CAP, int T>
 __device__ __noinline__ float ds_slice_max(const DsArgs& a, const __nv_bfloat16* z, int n) {
     float m = kDsLowest;
-    for (int j = threadIdx.x; j < n; j += T) m = fmaxf(m, a.sign * __bfloat162float(z[j]));
-    return CAP ? ds_arg<CAP>(a, a.sign * m) : m;
+    for (int j = threadIdx.x; j < n; j += T) {
+        const float v = __bfloat162float(z[j]);
+        m = fmaxf(m, CAP == kDsWideCap ? ds_arg<CAP>(a, v) : a.sign * v);  // (tanhf need not grow with its argument)
+    }
+    return CAP == kDsCap ? ds_arg<CAP>(a, a.sign * m) : m;
 }
-template <bool CAP, int T>
+template <int CAP, int T>
 __device__ __noinline__ float ds_slice_sum(const DsArgs& a, const __nv_bfloat16* z, int n, float m) {
     float s = 0.0f;
     for (int j = threadIdx.x; j < n; j += T) s += ds_rel<CAP>(a, ds_arg<CAP>(a, __bfloat162float(z[j])), m);
@@ -457,7 +488,7 @@ __device__ __forceinline__ void ds_reduce(const DsArgs& a, double* sum) {
 
 // T threads work on the slice (and kDsTeachers warps for the teacher), a chunk
 // is at most B vectors for each of them.
-template <bool GRAD, bool CAP, int T, int B>
+template <bool GRAD, int CAP, int T, int B>
 __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 ? 2 : 6) distill_kernel(const DsArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ DsShared sh;
@@ -548,7 +579,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
 #pragma unroll
         for (int k = 0; k < kDsAhead; ++k) ask();
         ds_cluster_wait();  // every block's shared memory can be stored to
-        float m = CAP ? -0.5f : 0.0f;  // the reference of sums
+        float m = CAP == kDsCap ? -0.5f : 0.0f;  // the reference of sums
         uint32_t again = 0u;           // exchanges for rows summed again
         float c = 0.0f;                // - the exponent of the one that the row being summed has
         uint64_t acc = 0u;
@@ -631,7 +662,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                         // asked for now, used at the next row
                         dloss = a.dloss != nullptr && i + 1 < rows ? a.dloss[(out_row + stride) * a.dloss_stride] : 1.0f;
                         olog = log2f(os);
-                        oc = log2f(og) - olog + (CAP ? 2.0f : 0.0f) - ds_exponent(a, om);
+                        oc = log2f(og) - olog + (CAP == kDsCap ? 2.0f : 0.0f) - ds_exponent(a, om);
                         fast = live && og > 0.0f && fabsf(oc) < kDsFast && !ds_far(a, om);
                         out_z = reinterpret_cast<uint4*>(a.dz + out_row * a.ld + c0) + tid;
                     }
@@ -645,7 +676,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                     } else {
 #pragma unroll 1
                         for (int b = 0; tid + b * T < len; ++b)
-                            __stcs(out_z + b * T, live ? ds_grad8_any<CAP>(a, out_at[b * T], om, olog, CAP ? 4.0f * og : og)
+                            __stcs(out_z + b * T, live ? ds_grad8_any<CAP>(a, out_at[b * T], om, olog, CAP == kDsCap ? 4.0f * og : og)
                                                        : make_uint4(0u, 0u, 0u, 0u));
                     }
                     out_z += chunk;

@@ -646,6 +646,11 @@ int validate_distill(const lora_distill_shape* sh) {
     return LORA_MLP_OK;
 }
 
+int ds_cap_form(const lora_distill_shape* sh) {
+    if (!(sh->softcap > 0.0f)) return kDsNoCap;
+    return sh->softcap / sh->temperature > kDsWide ? kDsWideCap : kDsCap;
+}
+
 DsArgs ds_args(const lora_distill_shape* sh, const void* logits, const void* values, const void* ids,
                const int64_t* labels, int* status) {
     DsArgs a{};
@@ -666,10 +671,17 @@ DsArgs ds_args(const lora_distill_shape* sh, const void* logits, const void* val
     a.scale = sh->logit_scale;
     a.sign = sh->logit_scale < 0.0f ? -1.0f : 1.0f;
     a.cap = sh->softcap;
+    a.form = ds_cap_form(sh);
     constexpr double kLog2e = 1.4426950408889634;
-    const double kn = (sh->softcap > 0.0f ? 2.0 * sh->softcap : 1.0 * sh->logit_scale) / sh->temperature;
+    double kn = 1.0 * sh->logit_scale / sh->temperature;
+    if (sh->softcap > 0.0f) {
+        const double ratio = 1.0 * sh->logit_scale / sh->softcap;
+        kn = (ds_cap_form(sh) == kDsWideCap ? 1.0 : 2.0 * sh->softcap) / sh->temperature;
+        a.cap2 = static_cast<float>(2.0 * ratio * kLog2e);
+        a.ratio2 = std::fabs(ratio) < 0x1p-60 ? 0x1p-60f : 1.0f;
+        a.ratio = static_cast<float>(ratio / a.ratio2);
+    }
     a.k = static_cast<float>(kn * kLog2e);
-    if (sh->softcap > 0.0f) a.cap2 = static_cast<float>(2.0 * a.scale / sh->softcap * kLog2e);
     a.status = status;
     a.wait_limit = 4000000000LL;  // about 2 s
     return a;
@@ -688,13 +700,12 @@ struct DsLaunch {
 // T threads for a slice, chunks of at most B vectors each.  The smallest
 // cluster whose blocks hold their slice and the chunks around it in shared
 // memory; a larger one where there are too few rows for the multiprocessors.
-template <int T, int B>
+template <bool GRAD, int T, int B>
 int plan_distill_by(const DsArgs& args, int sms, DsLaunch& l) {
     constexpr int64_t widest = T * B;  // vectors of a chunk
     l.a = args;
     DsArgs& a = l.a;
     l.threads = T + 32 * kDsTeachers;
-    const bool grad = a.dz != nullptr, cap = a.cap > 0.0f;
     const auto fixed = [&](int lc) {
         return kDsTeachers * ((static_cast<size_t>(a.K) + 3) / 4 * 4 * kDsEntryBytes + (size_t{4} << a.log_table)) +
                static_cast<size_t>(kDsDepth + 2) * (T / 32 * 8 << lc);
@@ -704,7 +715,7 @@ int plan_distill_by(const DsArgs& args, int sms, DsLaunch& l) {
     const auto chunk = [&](int lc) { return (slice(lc) + chunks(lc) - 1) / chunks(lc); };
     const auto most = [&](int lc) { return static_cast<int64_t>((kDsMaxSmem - fixed(lc)) / (chunk(lc) * 16)); };
     int lc = 0;
-    while ((1 << lc) < kDsMaxCluster && ((grad && chunks(lc) + 1 + kDsAhead > most(lc)) ||
+    while ((1 << lc) < kDsMaxCluster && ((GRAD && chunks(lc) + 1 + kDsAhead > most(lc)) ||
                                          ((a.N << lc) * 2 <= sms && chunks(lc) > 1)))
         ++lc;
     a.log_cluster = lc;
@@ -713,14 +724,15 @@ int plan_distill_by(const DsArgs& args, int sms, DsLaunch& l) {
     a.chunk = static_cast<int>(chunk(lc));
     // a chunk more than the row's, where there is room: the sums' way to the
     // other blocks is then hidden behind it
-    a.lag = a.chunks + (a.chunks > 1 && (!grad || a.chunks + 2 + kDsAhead <= most(lc)) ? 2 : 1);
-    a.slots = (grad ? a.lag : 0) + kDsAhead;
+    a.lag = a.chunks + (a.chunks > 1 && (!GRAD || a.chunks + 2 + kDsAhead <= most(lc)) ? 2 : 1);
+    a.slots = (GRAD ? a.lag : 0) + kDsAhead;
     if (a.slots > most(lc)) return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
     l.cluster = 1 << lc;
     l.smem = std::max(static_cast<size_t>(a.slots) * a.chunk * 16 + fixed(lc),
                       static_cast<size_t>(l.threads) * 12);  // 12: the reduction's sums and counts
-    l.kernel = grad ? (cap ? distill_kernel<true, true, T, B> : distill_kernel<true, false, T, B>)
-                    : (cap ? distill_kernel<false, true, T, B> : distill_kernel<false, false, T, B>);
+    l.kernel = a.form == kDsNoCap ? distill_kernel<GRAD, kDsNoCap, T, B>
+               : a.form == kDsCap ? distill_kernel<GRAD, kDsCap, T, B>
+                                  : distill_kernel<GRAD, kDsWideCap, T, B>;
     // As many clusters as run at once; each takes every so many-th row.
     int at_once = 0;
     STEP_TRY(resident_clusters(l.kernel, kDsMaxSmem, l.threads, l.smem, l.cluster, &at_once));
@@ -734,10 +746,11 @@ int plan_distill_by(const DsArgs& args, int sms, DsLaunch& l) {
 // threads, two an SM, 24 KB a chunk (107 us there; 111 with 16 KB).  Short rows
 // take blocks of 64 threads, so that a thread has work to overlap.
 int plan_distill(const DsArgs& a, int sms, DsLaunch& l) {
-    if (a.V <= 4096) return plan_distill_by<64, 4>(a, sms, l);
-    if (a.dz == nullptr) return plan_distill_by<256, 6>(a, sms, l);
-    const int rc = plan_distill_by<512, 3>(a, sms, l);
-    return rc == LORA_MLP_ERR_UNSUPPORTED_SHAPE ? plan_distill_by<512, 2>(a, sms, l) : rc;
+    const bool grad = a.dz != nullptr;
+    if (a.V <= 4096) return grad ? plan_distill_by<true, 64, 4>(a, sms, l) : plan_distill_by<false, 64, 4>(a, sms, l);
+    if (!grad) return plan_distill_by<false, 256, 6>(a, sms, l);
+    const int rc = plan_distill_by<true, 512, 3>(a, sms, l);
+    return rc == LORA_MLP_ERR_UNSUPPORTED_SHAPE ? plan_distill_by<true, 512, 2>(a, sms, l) : rc;
 }
 
 int launch_distill(const char* name, const DsLaunch& l, cudaStream_t st, bool after_own) {

@@ -147,3 +147,44 @@ def test_softcap_slope_far_from_zero(N, V, s, T):
     tol = (2.0 ** -8 + 2.0 ** -17) * np.abs(rd) + (T * dloss)[:, None] * slope * (q + P) * d + 2.0 ** -126
     bad = ~(np.abs(dz - rd) <= tol)
     assert not np.any(bad), (np.argwhere(bad)[:4], dz[bad][:4], rd[bad][:4], tol[bad][:4])
+
+
+WIDE = [(1e3, 1.0), (1e5, 1.0), (1e7, 1.0), (1e30, 1.0), (30.0, 0.01), (130.0, 1.0), (50.0, 0.3)]
+
+
+@pytest.mark.parametrize("N,V", SIZES)
+@pytest.mark.parametrize("s", [1.0, -0.25])
+@pytest.mark.parametrize("cap,T", WIDE)
+def test_caps_far_above_the_temperature_cost_no_precision(N, V, s, cap, T):
+    """Ordinary logits, and some near the cap, under caps of more than 128 temperatures.
+
+    t = cap tanh(s z / cap) is off by 2^-21 of itself (the quotient 2^-23, tanh 2^-22 by its two units in the last place,
+    the product 2^-24), so a logarithm of a probability by 2^-20 of the row's largest |t| / T beside the d of
+    test_gpu_distill.py without softcapping; nothing grows with the cap.  dt/dz as in the test before."""
+    rng = np.random.default_rng(V + 5)
+    z, values, ids = make(rng, N, V, 6, 2.0, abs(s))
+    z[::4] *= 5.0
+    if cap < 1e20:
+        z[1::4] = torch.from_numpy(rng.uniform(-3.0 * cap, 3.0 * cap, z[1::4].shape)).to(z.dtype) / abs(s)
+    dev, _ = padded(z)
+    dloss = rng.uniform(0.5, 1.5, N).astype(np.float32)
+    kw = dict(temperature=T, logit_scale=s, softcap=cap)
+    args = (dev, values.cuda(), ids.cuda())
+    loss = f64(api.distill_forward(*args, **kw))
+    dz = f64(api.distill_backward(*args, torch.from_numpy(dloss).cuda(), **kw))
+    z64 = f64(z)
+    cap, T = float(np.float32(cap)), float(np.float32(T))
+    rl, rd, q, P = ods.run(z64, f64(values), ids.numpy().astype(np.int64), dloss, None, T, s, cap)
+    x = cap * np.tanh(s * z64 / cap) / T
+    span = x.max(axis=1, keepdims=True) - x
+    d = 2e-5 + 2.0 ** -21 * span + 2.0 ** -20 * np.abs(x).max(axis=1, keepdims=True)
+    row = T * T * (np.max(d * (P > 0), axis=1) + 2.0 ** -20 * (np.max(span * (P > 0), axis=1) + 20.0))
+    slope = abs(s) / np.cosh(s * z64 / cap) ** 2
+    el = (2.0 ** -8 + 2.0 ** -17) * np.abs(rd) + (T * dloss)[:, None] * slope * (q + P) * d + 2.0 ** -126
+    for got, ref, tol in ((loss, rl, row), (dz, rd, el)):
+        bad = ~(np.abs(got - ref) <= tol)
+        assert not np.any(bad), (np.argwhere(bad)[:4], got[bad][:4], ref[bad][:4], tol[bad][:4])
+    _, dr = api.distill_loss(*args, reduction="sum", **kw)
+    unit = ods.run(z64, f64(values), ids.numpy().astype(np.int64), np.ones(N), None, T, s, cap)[1]
+    assert np.all(np.abs(f64(dr) - unit) <= el / dloss[:, None] + 2.0 ** -126)
+    assert api.step_device_status() == 0
