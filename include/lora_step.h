@@ -38,6 +38,14 @@ int lora_step_timing_collect(lora_mlp_kernel_time* out, int max, int* count);
 /* Kernels of these operators launched in this process (all devices). */
 int64_t lora_step_launch_count(void);
 
+/* Test hook for the failure path, as lora_mlp_debug_force_timeout is for the
+ * others: while enabled, no wait of the distillation's kernels is ever over, and
+ * each gives up after `wait_cycles` SM cycles.  The kernels then return, with
+ * LORA_MLP_ERR_DEVICE_TIMEOUT for lora_step_device_status and outputs that are
+ * not complete.  enable = 0 restores normal operation.  Process-wide; not for
+ * production. */
+int lora_step_debug_force_timeout(int enable, int64_t wait_cycles);
+
 #ifdef __cplusplus
 }
 #endif

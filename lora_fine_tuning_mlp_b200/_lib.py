@@ -74,6 +74,7 @@ STEP_SYMBOLS = (
     "lora_step_timing_enable",
     "lora_step_timing_collect",
     "lora_step_launch_count",
+    "lora_step_debug_force_timeout",
     "lora_embedding_forward",
     "lora_embedding_sizes",
     "lora_embedding_backward",
@@ -214,6 +215,7 @@ def lib() -> ctypes.CDLL:
             L.lora_step_timing_enable.argtypes = [ctypes.c_int]
             L.lora_step_timing_collect.argtypes = L.lora_mlp_timing_collect.argtypes
             L.lora_step_launch_count.argtypes = []
+            L.lora_step_debug_force_timeout.argtypes = [ctypes.c_int, i64]
             L.lora_embedding_forward.argtypes = [i64, i64, i64, ctypes.c_float, vp, vp, vp, vp]
             L.lora_embedding_sizes.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
             L.lora_embedding_backward.argtypes = [i64, i64, i64, ctypes.c_float, i64, ctypes.c_int, vp, vp, vp, vp, sz,
@@ -338,6 +340,10 @@ def debug_force_timeout(enable: bool, wait_cycles: int = 0) -> None:
 
 def launch_count() -> int:
     return int(lib().lora_mlp_launch_count()) + int(lib().lora_step_launch_count())
+
+
+def step_debug_force_timeout(enable: bool, wait_cycles: int = 0) -> None:
+    check(lib().lora_step_debug_force_timeout(1 if enable else 0, int(wait_cycles)), "lora_step_debug_force_timeout")
 
 
 def step_device_status(stream) -> int:

@@ -80,6 +80,7 @@ struct DsArgs {
     int lag;     // chunks between a chunk's two uses
     int slots;   // chunks of the ring
     long long wait_limit;  // SM cycles that a wait may take before the kernel gives up
+    int force_timeout;     // test hook: no wait is ever over
     const void *values, *ids;
     int values_f32, ids_i64;
     const long long* labels;  // may be null
@@ -277,11 +278,11 @@ __device__ __forceinline__ V ds_look(const V* p) {
 // where it ran out here or for another of the block's warps.
 template <class F>
 __device__ __forceinline__ bool ds_wait(const DsArgs& a, DsShared& sh, F here) {
-    if (__all_sync(0xffffffffu, here())) return true;
+    if (!a.force_timeout && __all_sync(0xffffffffu, here())) return true;
     const long long begin = clock64();
     for (;;) {
         __nanosleep(300);  // polls without a pause take issue slots from the warps that work: 3 % of the kernel's time
-        if (__all_sync(0xffffffffu, here())) return true;
+        if (!a.force_timeout && __all_sync(0xffffffffu, here())) return true;
         const bool stop = ds_look(&sh.gave_up) != 0 || clock64() - begin > a.wait_limit;
         if (__any_sync(0xffffffffu, stop)) {
             if (ds_look(&sh.gave_up) == 0) atomicExch(a.status, kDsTimeout);

@@ -35,6 +35,10 @@ __device__ int g_step_status;
 
 std::atomic<int64_t> g_launches{0};
 
+constexpr long long kWaitLimitCycles = 4000000000LL;  // about 2 s
+std::atomic<long long> g_wait_limit{kWaitLimitCycles};
+std::atomic<int> g_force_timeout{0};
+
 // ----------------------------------------------------------------------------- device info
 struct DevInfo {
     bool checked, ok;
@@ -273,6 +277,13 @@ int lora_step_timing_collect(lora_mlp_kernel_time* out, int max, int* count) {
 }
 
 int64_t lora_step_launch_count(void) { return g_launches.load(); }
+
+int lora_step_debug_force_timeout(int enable, int64_t wait_cycles) {
+    if (enable && wait_cycles < 1) return LORA_MLP_ERR_INVALID_ARG;
+    g_wait_limit.store(enable ? static_cast<long long>(wait_cycles) : kWaitLimitCycles);
+    g_force_timeout.store(enable ? 1 : 0);
+    return LORA_MLP_OK;
+}
 
 }  // extern "C"
 
@@ -683,7 +694,8 @@ DsArgs ds_args(const lora_distill_shape* sh, const void* logits, const void* val
     }
     a.k = static_cast<float>(kn * kLog2e);
     a.status = status;
-    a.wait_limit = 4000000000LL;  // about 2 s
+    a.wait_limit = g_wait_limit.load();
+    a.force_timeout = g_force_timeout.load();
     return a;
 }
 
