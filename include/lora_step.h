@@ -27,7 +27,8 @@ extern "C" {
  * device: LORA_MLP_OK, or LORA_MLP_ERR_INVALID_ARG after a token id, position
  * or teacher id outside its range (each header says what such an entry's
  * result is), or LORA_MLP_ERR_DEVICE_TIMEOUT after a bounded wait between
- * blocks ran out (lora_distill.h).  Synchronises `stream`. */
+ * blocks ran out (lora_distill.h); after both, the latter.  Synchronises
+ * `stream`. */
 int lora_step_device_status(void* stream, int* status);
 
 /* Kernel timing of these operators, as lora_mlp_timing_enable and

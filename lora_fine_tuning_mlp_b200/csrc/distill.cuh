@@ -285,7 +285,7 @@ __device__ __forceinline__ bool ds_wait(const DsArgs& a, DsShared& sh, F here) {
         if (!a.force_timeout && __all_sync(0xffffffffu, here())) return true;
         const bool stop = ds_look(&sh.gave_up) != 0 || clock64() - begin > a.wait_limit;
         if (__any_sync(0xffffffffu, stop)) {
-            if (ds_look(&sh.gave_up) == 0) atomicExch(a.status, kDsTimeout);
+            if (ds_look(&sh.gave_up) == 0) atomicMin(a.status, kDsTimeout);
             *static_cast<volatile int*>(&sh.gave_up) = 1;
             return false;
         }
@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                 sum = ds_warp_sum(sum);
                 if (lane == 0) a.loss[row] = t.bad ? __int_as_float(0x7fc00000) : (t.live ? a.T * a.T * sum : 0.0f);
             }
-            if (t.bad && rank == 0 && lane == 0) atomicExch(a.status, kStatusBad);
+            if (t.bad && rank == 0 && lane == 0) atomicMin(a.status, kStatusBad);
             if (GRAD) {
                 const float g = upstream(row), log_s = log2f(s);
                 const uint32_t done = ds_smem(&sh.done[warp - W]), parity = static_cast<uint32_t>(i / kDsTeachers) & 1u;

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kEmbThreads) embed_fwd_kernel(const EmbFwdArgs
     uint4* o = reinterpret_cast<uint4*>(a.out) + t * a.nv;
     const int step = 1 << a.log_tpr;
     if (id < 0 || id >= a.V) {
-        if (lane == 0) atomicExch(a.status, kStatusBad);
+        if (lane == 0) atomicMin(a.status, kStatusBad);
         for (int j = lane; j < a.nv; j += step) o[j] = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
         return;
     }
@@ -107,7 +107,7 @@ struct SortArgs {
 __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, long long id) {
     if (id == a.padding && a.padding >= 0) return static_cast<uint32_t>(a.V);
     if (id < 0 || id >= a.V) {
-        atomicExch(a.status, kStatusBad);
+        atomicMin(a.status, kStatusBad);
         return static_cast<uint32_t>(a.V);
     }
     return static_cast<uint32_t>(id);

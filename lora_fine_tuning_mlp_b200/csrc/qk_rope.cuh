@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kQkThreads, NORM ? 4 : 8) qk_rope_kernel(const
     QkAngles ang{};
     const auto angles = [&](long long at) {
         bad = at < 0 || at >= a.P;
-        if (bad && slot == 0) atomicExch(a.status, kStatusBad);
+        if (bad && slot == 0) atomicMin(a.status, kStatusBad);
         turns = slot < a.nrot && !bad;
         if (turns) ang = qk_angles(a, at, slot);
     };
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBwdBlocksPerSm) qk_rope_bwd_ker
             for (int u = 0; u < U; ++u) {
                 if (FLAT || u == 0) {
                     bad[u] = p[u] < 0 || p[u] >= a.P;
-                    if (bad[u] && slot == 0) atomicExch(a.status, kStatusBad);
+                    if (bad[u] && slot == 0) atomicMin(a.status, kStatusBad);
                     if (slot < a.nrot && !bad[u]) ang = qk_angles(a, p[u], slot);
                 } else {
                     bad[u] = bad[0];

@@ -6,6 +6,8 @@
 namespace lmlp {
 namespace step {
 
+// Of the status word, which keeps the lowest: a wait that ran out
+// (LORA_MLP_ERR_DEVICE_TIMEOUT, -7) is not hidden by an id out of its range.
 constexpr int kStatusBad = -1;  // LORA_MLP_ERR_INVALID_ARG
 
 __device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
