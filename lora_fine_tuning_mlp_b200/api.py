@@ -6,6 +6,7 @@ if the CUDA library is missing or the device is not a B200 the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -146,13 +147,27 @@ class Workspace:
         return self.buf
 
 
+def _allocate(stream, make):
+    """make(), memory for a call that runs on `stream`.  It comes from that stream's part of the allocator: what the
+    current stream's part hands out may still be in use by work queued there, which `stream` does not wait for.  The
+    caller goes on with it on the current stream, which the allocator is told."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(here)
+    return t
+
+
 def _scratch(workspace, nbytes: int, device, stream):
-    """The workspace's buffer, or one for this call alone, which the allocator then keeps for `stream` too."""
-    if workspace is not None:
-        return workspace.get(nbytes, device)
-    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    """The workspace's buffer, or one for this call alone."""
+    if workspace is None:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    buf = _allocate(stream, lambda: workspace.get(nbytes, device))
     if stream is not None:
-        buf.record_stream(stream)
+        buf.record_stream(stream)  # it may come from an earlier call on another one
     return buf
 
 
@@ -757,6 +772,9 @@ class CrossEntropyFunction(torch.autograd.Function):
 
 
 # ----------------------------------------------------------------------------- token embedding
+#
+# From here on, a call with a `stream` allocates for that stream.  Its inputs are the caller's: they are ready for
+# `stream` when the call is made, and stay until `stream` has read them (Tensor.record_stream).
 
 
 def embedding_forward(ids: torch.Tensor, E: torch.Tensor, *, scale: float = 1.0, out=None, stream=None):
@@ -767,7 +785,7 @@ def embedding_forward(ids: torch.Tensor, E: torch.Tensor, *, scale: float = 1.0,
     if ids.dim() != 1 or E.dim() != 2:
         raise ValueError("ids must be [N] and E [V, d]")
     (N,), (V, d) = ids.shape, E.shape
-    out = E.new_empty((N, d)) if out is None else _need(out, "out", BF16, (N, d))
+    out = _allocate(stream, lambda: E.new_empty((N, d))) if out is None else _need(out, "out", BF16, (N, d))
     _lib.check(_lib.embedding_forward(N, V, d, scale, _p(ids), _p(E), _p(out), _stream(stream)),
                "lora_embedding_forward")
     return out
@@ -789,7 +807,10 @@ def embedding_backward(dOut: torch.Tensor, ids: torch.Tensor, V: int, *, scale: 
     if padding_idx is not None and not 0 <= padding_idx < V:
         raise ValueError(f"padding_idx must be in [0, {V})")
     dev = dOut.device
-    dE = torch.empty((V, d), dtype=dtype, device=dev) if dE is None else _need(dE, "dE", dtype, (V, d))
+    if dE is None:
+        dE = _allocate(stream, lambda: torch.empty((V, d), dtype=dtype, device=dev))
+    else:
+        _need(dE, "dE", dtype, (V, d))
     ws = _scratch(workspace, _lib.embedding_sizes(N, V, d), dev, stream)
     _lib.check(_lib.embedding_backward(N, V, d, scale, -1 if padding_idx is None else padding_idx, kind, _p(ids),
                                        _p(dOut), _p(dE), _p(ws), ws.numel(), _stream(stream)),
@@ -864,11 +885,11 @@ def _heads(t, name, shape=None, written=False):
     return _lib.QKView(t.data_ptr(), sb, ss, sh)
 
 
-def _heads_out(t, name, like):
+def _heads_out(t, name, like, stream):
     """(t or a new contiguous tensor of `like`'s shape, its view)."""
     if t is not None:
         return t, _heads(t, name, like.shape, True)
-    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    t = _allocate(stream, lambda: torch.empty_like(like, memory_format=torch.contiguous_format))
     S, H, D = t.shape[-3:]
     return t, _lib.QKView(t.data_ptr(), S * H * D, H * D, D)
 
@@ -910,8 +931,8 @@ def qk_norm_rope_forward(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, si
     [B, S] or [S], else 0 .. S-1.  Pairs are (i, i + rot/2), or (2i, 2i + 1) with interleaved; elements from rot on
     do not turn.  q, k and given outputs may be strided views; new outputs are contiguous."""
     shape, vq, vk, rest = _qk_call(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved)
-    q_out, oq = _heads_out(q_out, "q_out", q)
-    k_out, ok = _heads_out(k_out, "k_out", k)
+    q_out, oq = _heads_out(q_out, "q_out", q, stream)
+    k_out, ok = _heads_out(k_out, "k_out", k, stream)
     _lib.check(_lib.qk_rope_forward(shape, vq, vk, *rest, oq, ok, _stream(stream)), "lora_qk_rope_forward")
     return q_out, k_out
 
@@ -924,11 +945,11 @@ def qk_norm_rope_backward(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, s
     gradients are fp32 [D], None without gains or with gain_grads=False (frozen gains)."""
     shape, vq, vk, rest = _qk_call(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved)
     vdq_out, vdk_out = _heads(dq_out, "dq_out", q.shape), _heads(dk_out, "dk_out", k.shape)
-    dq, vdq = _heads_out(dq, "dq", q)
-    dk, vdk = _heads_out(dk, "dk", k)
+    dq, vdq = _heads_out(dq, "dq", q, stream)
+    dk, vdk = _heads_out(dk, "dk", k, stream)
     dgq = dgk = ws = None
     if q_gain is not None and gain_grads:
-        dgq, dgk = q.new_empty((2, shape.D), dtype=torch.float32).unbind(0)
+        dgq, dgk = _allocate(stream, lambda: q.new_empty((2, shape.D), dtype=torch.float32)).unbind(0)
         ws = _scratch(workspace, _lib.qk_rope_sizes(shape), q.device, stream)
     _lib.check(_lib.qk_rope_backward(shape, vq, vk, *rest, vdq_out, vdk_out, vdq, vdk, _p(dgq), _p(dgk), _p(ws),
                                      0 if ws is None else ws.numel(), _stream(stream)), "lora_qk_rope_backward")
@@ -998,12 +1019,12 @@ def _distill_call(logits, values, ids, labels, temperature, logit_scale, softcap
     return shape, (_p(logits), _p(values), _p(ids), _p(labels))
 
 
-def _distill_out(logits, out, inplace):
+def _distill_out(logits, out, inplace, stream):
     # the gradient is written with the logits' row stride, as in ce_backward
     if inplace:
         return logits
     if out is None:
-        return logits.new_empty_strided(logits.shape, logits.stride())
+        return _allocate(stream, lambda: logits.new_empty_strided(logits.shape, logits.stride()))
     if out.shape != logits.shape or out.stride() != logits.stride() or out.dtype != BF16 or not out.is_cuda:
         raise ValueError("out must have the logits' shape, strides and dtype")
     return out
@@ -1018,7 +1039,7 @@ def distill_forward(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_
     label (int64 [N], optional) is ignore_index and for rows without an entry."""
     shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
                                 ignore_index)
-    loss = logits.new_empty((shape.N,), dtype=torch.float32)
+    loss = _allocate(stream, lambda: logits.new_empty((shape.N,), dtype=torch.float32))
     _lib.check(_lib.distill_forward(shape, *ptrs, _p(loss), _stream(stream)), "lora_distill_forward")
     return loss
 
@@ -1031,7 +1052,7 @@ def distill_backward(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher
     shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
                                 ignore_index)
     _need(dloss, "dloss", torch.float32, (shape.N,))
-    out = _distill_out(logits, out, inplace)
+    out = _distill_out(logits, out, inplace, stream)
     _lib.check(_lib.distill_backward(shape, *ptrs, _p(dloss), _p(out), _stream(stream)), "lora_distill_backward")
     return out
 
@@ -1049,8 +1070,8 @@ def distill_loss(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ids
         raise ValueError("reduction must be 'sum' or 'mean'")
     shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
                                 ignore_index)
-    out = logits.new_empty((2,), dtype=torch.float32)
-    dlogits = _distill_out(logits, grad_out, inplace) if with_grad else None
+    out = _allocate(stream, lambda: logits.new_empty((2,), dtype=torch.float32))
+    dlogits = _distill_out(logits, grad_out, inplace, stream) if with_grad else None
     ws = _scratch(workspace, _lib.distill_sizes(shape), logits.device, stream)
     _lib.check(_lib.distill_loss(shape, *ptrs, red, _p(out), _p(dlogits), _p(ws), ws.numel(), _stream(stream)),
                "lora_distill_loss")
@@ -1068,7 +1089,7 @@ def distill_backward_reduced(logits: torch.Tensor, teacher_logits: torch.Tensor,
     _need(fwd_out, "fwd_out", torch.float32, (2,))
     if dout.numel() != 1 or dout.dtype != torch.float32 or not dout.is_cuda:
         raise TypeError("dout must be one fp32 CUDA element")
-    out = _distill_out(logits, out, inplace)
+    out = _distill_out(logits, out, inplace, stream)
     _lib.check(_lib.distill_backward_reduced(shape, *ptrs, _p(dout), _p(fwd_out), _p(out), _stream(stream)),
                "lora_distill_backward_reduced")
     return out
