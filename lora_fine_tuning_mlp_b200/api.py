@@ -3,10 +3,15 @@
 PyTorch provides device memory and the current stream; every step of the
 LoRA SwiGLU MLP and of the LoRA linear runs in the library's sm_100a kernels.  There is no fallback:
 if the CUDA library is missing or the device is not a B200 the call raises.
+
+A call with a `stream` runs on that stream and allocates for it.  Its inputs
+are the caller's: they are ready for the stream when the call is made, and stay
+until the stream has read them (Tensor.record_stream).
 """
 from __future__ import annotations
 
 import contextlib
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -171,11 +176,39 @@ def _scratch(workspace, nbytes: int, device, stream):
     return buf
 
 
+def _tensors(x):
+    """The tensors of a call's results."""
+    if hasattr(x, "record_stream"):
+        yield x
+    elif x is not None:
+        for y in x.values() if isinstance(x, dict) else x if isinstance(x, (tuple, list)) else vars(x).values():
+            yield from _tensors(y)
+
+
+def _allocates_for_its_stream(call):
+    """A call with a `stream` allocates as in _allocate and _scratch."""
+    @functools.wraps(call)
+    def on_its_stream(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        here = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            results = call(*args, stream=stream, **kw)
+        for t in _tensors(results):
+            t.record_stream(here)
+        if kw.get("workspace") is not None:
+            for s in (here, stream):
+                kw["workspace"].buf.record_stream(s)
+        return results
+    return on_its_stream
+
+
 def sizes(w: MLPWeights, N: int):
     """(forward workspace, backward workspace, saved) byte counts."""
     return _lib.sizes(w.shape(N))
 
 
+@_allocates_for_its_stream
 def forward(X: torch.Tensor, w: MLPWeights, *, out=None, workspace: Workspace | None = None, stream=None):
     """out = MLP(X).  Returns (out, Saved)."""
     N, d = X.shape
@@ -194,6 +227,7 @@ def forward(X: torch.Tensor, w: MLPWeights, *, out=None, workspace: Workspace | 
     return out, Saved(g, u, lowrank)
 
 
+@_allocates_for_its_stream
 def backward(X: torch.Tensor, w: MLPWeights, saved: Saved, dOut: torch.Tensor, *, dX=None, grads=None,
              workspace: Workspace | None = None, stream=None):
     """Returns (dX, {dAg, dBg, dAu, dBu, dAd, dBd})."""
@@ -218,7 +252,7 @@ def dequant_int4(packed: torch.Tensor, scales: torch.Tensor, stream=None) -> tor
     rows, half = packed.shape
     _need(packed, "packed", torch.uint8)
     _need(scales, "scales", torch.float16, (rows, 2 * half // 64))
-    w = torch.empty((rows, 2 * half), dtype=BF16, device=packed.device)
+    w = _allocate(stream, lambda: torch.empty((rows, 2 * half), dtype=BF16, device=packed.device))
     _lib.check(_lib.dequant_int4(_p(packed), _p(scales), rows, 2 * half, _p(w), _stream(stream)),
                "lora_mlp_dequant_int4")
     return w
@@ -231,7 +265,7 @@ def dequant_fp8(codes: torch.Tensor, scales: torch.Tensor, stream=None) -> torch
     if codes.dtype not in (torch.uint8, torch.float8_e4m3fn):
         raise TypeError("codes must be float8_e4m3fn or uint8")
     _need(scales, "scales", torch.float32, (rows, cols // 64))
-    w = torch.empty((rows, cols), dtype=BF16, device=codes.device)
+    w = _allocate(stream, lambda: torch.empty((rows, cols), dtype=BF16, device=codes.device))
     _lib.check(_lib.dequant_fp8(_p(codes), _p(scales), rows, cols, _p(w), _stream(stream)), "lora_mlp_dequant_fp8")
     return w
 
@@ -444,6 +478,7 @@ def linear_sizes(w: LinearWeights, N: int):
     return _lib.lin_sizes(w.shape(N))
 
 
+@_allocates_for_its_stream
 def linear_forward(X: torch.Tensor, w: LinearWeights, *, Y=None, workspace: Workspace | None = None,
                    stream=None):
     """Y = X (W + s B A)^T.  Returns (Y, saved) where saved is the opaque
@@ -462,6 +497,7 @@ def linear_forward(X: torch.Tensor, w: LinearWeights, *, Y=None, workspace: Work
     return Y, saved
 
 
+@_allocates_for_its_stream
 def linear_backward(X: torch.Tensor, w: LinearWeights, saved: torch.Tensor, dY: torch.Tensor, *, dX=None,
                     dA=None, dB=None, workspace: Workspace | None = None, stream=None):
     """Returns (dX, dA, dB)."""
@@ -518,6 +554,7 @@ def linear_weights_from_host(inp: dict, alpha: float, device="cuda") -> LinearWe
 # ----------------------------------------------------------------------------- RMSNorm and the pre-norm block
 
 
+@_allocates_for_its_stream
 def rmsnorm_forward(x: torch.Tensor, gamma: torch.Tensor, eps: float, *, stream=None):
     """Returns (y, rstd): y = RMSNorm(x) * gamma (bf16), rstd fp32 [N]."""
     N, d = x.shape
@@ -530,6 +567,7 @@ def rmsnorm_forward(x: torch.Tensor, gamma: torch.Tensor, eps: float, *, stream=
     return y, rstd
 
 
+@_allocates_for_its_stream
 def rmsnorm_backward(x: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor, *, stream=None):
     N, d = x.shape
     _need(x, "x", BF16)
@@ -569,12 +607,13 @@ def fold_gamma(w: MLPWeights, gamma: torch.Tensor, stream=None) -> MLPWeights:
         raise ValueError("gamma folds into bf16 frozen weights only")
     w.validate()
     _need(gamma, "gamma", BF16, (w.d,))
-    Wg, Wu = torch.empty_like(w.Wg), torch.empty_like(w.Wu)
+    Wg, Wu = (_allocate(stream, lambda t=t: torch.empty_like(t)) for t in (w.Wg, w.Wu))
     _lib.check(_lib.block_fold_gamma(w.shape(1), w.c_struct(), _p(gamma), _p(Wg), _p(Wu), _stream(stream)),
                "lora_mlp_block_fold_gamma")
     return MLPWeights(Wg=Wg, Wu=Wu, Wd=w.Wd, Ag=w.Ag, Bg=w.Bg, Au=w.Au, Bu=w.Bu, Ad=w.Ad, Bd=w.Bd, alpha=w.alpha)
 
 
+@_allocates_for_its_stream
 def block_forward(X: torch.Tensor, w: MLPWeights, gamma: torch.Tensor, eps: float, *, out=None,
                   workspace: Workspace | None = None, stream=None, folded: bool = False):
     """out = MLP(RMSNorm(X) * gamma).  Returns (out, Saved); Saved.lowrank
@@ -598,6 +637,7 @@ def block_forward(X: torch.Tensor, w: MLPWeights, gamma: torch.Tensor, eps: floa
     return out, Saved(g, u, saved)
 
 
+@_allocates_for_its_stream
 def block_backward(X: torch.Tensor, w: MLPWeights, gamma: torch.Tensor, saved: Saved, dOut: torch.Tensor, *,
                    dX=None, grads=None, workspace: Workspace | None = None, stream=None, folded: bool = False):
     """Returns (dX, {dAg, dBg, dAu, dBu, dAd, dBd}) for the block input X.
@@ -655,6 +695,7 @@ def _ce_shape(logits: torch.Tensor, logit_scale: float, softcap: float, ignore_i
     return _lib.make_ce_shape(N, V, logits.stride(0), logit_scale, softcap, ignore_index)
 
 
+@_allocates_for_its_stream
 def ce_forward(logits: torch.Tensor, labels: torch.Tensor, *, logit_scale: float = 1.0, softcap: float = 0.0,
                ignore_index: int = -100, workspace: Workspace | None = None, stream=None):
     """Per-row cross-entropy of bf16 logits [N, V] (row stride a multiple of
@@ -672,6 +713,7 @@ def ce_forward(logits: torch.Tensor, labels: torch.Tensor, *, logit_scale: float
     return loss, lse
 
 
+@_allocates_for_its_stream
 def ce_backward(logits: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor, dloss: torch.Tensor, *,
                 logit_scale: float = 1.0, softcap: float = 0.0, ignore_index: int = -100, out=None,
                 inplace: bool = False, stream=None):
@@ -695,6 +737,7 @@ def ce_backward(logits: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor, d
     return out
 
 
+@_allocates_for_its_stream
 def ce_loss(logits: torch.Tensor, labels: torch.Tensor, *, reduction: str = "mean", logit_scale: float = 1.0,
             softcap: float = 0.0, ignore_index: int = -100, workspace: Workspace | None = None, stream=None):
     """The cross-entropy reduced over the rows, computed by the library:
@@ -716,6 +759,7 @@ def ce_loss(logits: torch.Tensor, labels: torch.Tensor, *, reduction: str = "mea
     return out, lse
 
 
+@_allocates_for_its_stream
 def ce_backward_reduced(logits: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor, dout: torch.Tensor,
                         fwd_out: torch.Tensor, *, logit_scale: float = 1.0, softcap: float = 0.0,
                         ignore_index: int = -100, out=None, inplace: bool = False, stream=None):
@@ -772,9 +816,6 @@ class CrossEntropyFunction(torch.autograd.Function):
 
 
 # ----------------------------------------------------------------------------- token embedding
-#
-# From here on, a call with a `stream` allocates for that stream.  Its inputs are the caller's: they are ready for
-# `stream` when the call is made, and stay until `stream` has read them (Tensor.record_stream).
 
 
 def embedding_forward(ids: torch.Tensor, E: torch.Tensor, *, scale: float = 1.0, out=None, stream=None):

@@ -1,5 +1,5 @@
-"""Calls of the operators around the dense layers on a stream of their own beside calls on the current one, with nothing
-between them that waits: each gives the bits of a call by itself."""
+"""Calls on a stream of their own beside calls on the current one, with nothing between them that waits: each
+gives the bits of a call by itself."""
 import pytest
 import torch
 
@@ -99,3 +99,44 @@ def test_a_call_on_a_side_stream_of_a_capture():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(t, r) for t, r in zip(got, ref))
+
+
+def test_dense_layers_norms_and_losses_beside_the_current_stream():
+    def make(seed):
+        g = torch.Generator().manual_seed(seed)
+
+        def rand(*shape):
+            return (torch.randn(*shape, generator=g) * shape[-1] ** -0.5).to(BF16).cuda()
+
+        n, d, f, r = 1024, 512, 1024, 8
+        w = api.MLPWeights(rand(f, d), rand(f, d), rand(d, f), rand(r, d), rand(f, r), rand(r, d), rand(f, r),
+                           rand(r, f), rand(d, r), alpha=16.0)
+        lw = api.LinearWeights(W=rand(f, d), A=rand(r, d), B=rand(f, r), alpha=16.0)
+        x, dy, dz, gamma = rand(n, d), rand(n, d), rand(n, f), rand(d)
+        labels, ones = torch.randint(0, f, (n,), generator=g).cuda(), torch.ones(n, device="cuda")
+
+        def calls(stream):
+            kw = {"stream": stream}
+            out, saved = api.forward(x, w, **kw)
+            dx, grads = api.backward(x, w, saved, dy, **kw)
+            bo, bsaved = api.block_forward(x, w, gamma, 1e-5, **kw)
+            bx, bgrads = api.block_backward(x, w, gamma, bsaved, dy, **kw)
+            y, lsaved = api.linear_forward(x, lw, **kw)
+            h, rstd = api.rmsnorm_forward(x, gamma, 1e-5, **kw)
+            loss, lse = api.ce_loss(dz, labels, **kw)
+            return [out, dx, *grads.values(), bo, bx, *bgrads.values(), y,
+                    *api.linear_backward(x, lw, lsaved, dz, **kw), h,
+                    api.rmsnorm_backward(x, gamma, rstd, dy, **kw), loss,
+                    api.ce_backward(dz, labels, lse, ones, **kw)]
+        return calls
+
+    a, b = make(1), make(2)
+    ref = {x: [t.clone() for t in x(None)] for x in (a, b)}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    kept = []
+    for i in range(6):
+        kept.append((a, a(None)))
+        kept.append((b, b(side)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, r) for x, got in kept for t, r in zip(got, ref[x]))

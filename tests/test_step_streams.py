@@ -1,6 +1,6 @@
-"""Whose memory a call of the operators around the dense layers allocates where it runs on a stream of its own.  The
-kernels of a call with `stream` wait for nothing that is queued on the current stream, so their buffers must not come
-from the current stream's part of the allocator.  Fakes instead of a GPU."""
+"""Whose memory a call allocates where it runs on a stream of its own.  The kernels of a call with
+`stream` wait for nothing that is queued on the current stream, so their buffers must not come from the current
+stream's part of the allocator.  Fakes instead of a GPU."""
 import contextlib
 
 import pytest
@@ -64,3 +64,24 @@ def test_results(streams):
     out = api._allocate(other, lambda: torch.empty(4))
     assert out.allocated is other and here in out.recorded
     assert api._allocate(None, lambda: torch.empty(4)).allocated is here
+
+
+def test_calls_of_the_dense_layers(streams):
+    here, other = streams
+    ws = api.Workspace()
+
+    @api._allocates_for_its_stream
+    def call(n, *, workspace=None, stream=None):
+        return torch.empty(n), {"a": torch.empty(n), "none": None}, workspace.get(n, None)
+
+    y, grads, buf = call(4, workspace=ws, stream=other)
+    assert all(t.allocated is other and here in t.recorded for t in (y, grads["a"], buf))
+    y, grads, again = call(4, workspace=ws)
+    assert y.allocated is here and not y.recorded and again is buf
+
+
+@pytest.mark.parametrize("name", ["forward", "backward", "linear_forward", "linear_backward", "rmsnorm_forward",
+                                  "rmsnorm_backward", "block_forward", "block_backward", "ce_forward", "ce_backward",
+                                  "ce_loss", "ce_backward_reduced"])
+def test_every_one_of_them_does(name):
+    assert getattr(api, name).__name__ == name and hasattr(getattr(api, name), "__wrapped__")
