@@ -26,8 +26,10 @@
  * and gradients are bf16 views: 16-byte aligned, strides of batch, position
  * and head in elements, multiples of 8, the D elements of a head next to each
  * other.  So parts of one projection's output and heads-first tensors need no
- * copy.  Views that are written must not overlap themselves or a view that is
- * read.  cos and sin are fp32 [P, rot/2], 16-byte aligned; gains bf16 [D],
+ * copy.  A view that is written does not overlap itself: in ascending order,
+ * each of its strides is at least what the axes before it span.  It may be
+ * exactly the view of the same heads that is read (q_out = q; dq = dq_out, or dq =
+ * q), and overlaps no other.  cos and sin are fp32 [P, rot/2], 16-byte aligned; gains bf16 [D],
  * 16-byte aligned; their gradients fp32 [D], 4-byte aligned.  positions are
  * int64, 8-byte aligned: entry b * position_stride + s, in [0, P); NULL means
  * position s.  B, S, Hq, Hk >= 1; D and rot multiples of 16,
@@ -70,8 +72,8 @@ int lora_qk_rope_forward(const lora_qk_shape* shape, const lora_qk_view* q, cons
                          const int64_t* positions, const lora_qk_view* q_out, const lora_qk_view* k_out,
                          void* stream);
 
-/* Workspace bytes of lora_qk_rope_backward (0 without gains' gradients).  Host
- * only. */
+/* Workspace bytes of lora_qk_rope_backward for the gains' gradients; a call
+ * without them needs none (workspace may be NULL).  Host only. */
 int lora_qk_rope_sizes(const lora_qk_shape* shape, size_t* workspace_bytes);
 
 /* dq, dk (views) and, where dq_gain and dk_gain are not NULL, the gains'

@@ -10,7 +10,6 @@ until the stream has read them (Tensor.record_stream).
 """
 from __future__ import annotations
 
-import contextlib
 import functools
 from dataclasses import dataclass
 
@@ -152,15 +151,15 @@ class Workspace:
         return self.buf
 
 
-def _allocate(stream, make):
-    """make(), memory for a call that runs on `stream`.  It comes from that stream's part of the allocator: what the
+def _allocate(stream, make, *args, **kw):
+    """make(*args, **kw), memory for a call that runs on `stream`.  It comes from that stream's part of the allocator: what the
     current stream's part hands out may still be in use by work queued there, which `stream` does not wait for.  The
     caller goes on with it on the current stream, which the allocator is told."""
     if stream is None:
-        return make()
+        return make(*args, **kw)
     here = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
-        t = make()
+        t = make(*args, **kw)
     t.record_stream(here)
     return t
 
@@ -168,9 +167,11 @@ def _allocate(stream, make):
 def _scratch(workspace, nbytes: int, device, stream):
     """The workspace's buffer, or one for this call alone."""
     if workspace is None:
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        if stream is None:
             return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    buf = _allocate(stream, lambda: workspace.get(nbytes, device))
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    buf = _allocate(stream, workspace.get, nbytes, device)
     if stream is not None:
         buf.record_stream(stream)  # it may come from an earlier call on another one
     return buf
@@ -252,7 +253,7 @@ def dequant_int4(packed: torch.Tensor, scales: torch.Tensor, stream=None) -> tor
     rows, half = packed.shape
     _need(packed, "packed", torch.uint8)
     _need(scales, "scales", torch.float16, (rows, 2 * half // 64))
-    w = _allocate(stream, lambda: torch.empty((rows, 2 * half), dtype=BF16, device=packed.device))
+    w = _allocate(stream, torch.empty, (rows, 2 * half), dtype=BF16, device=packed.device)
     _lib.check(_lib.dequant_int4(_p(packed), _p(scales), rows, 2 * half, _p(w), _stream(stream)),
                "lora_mlp_dequant_int4")
     return w
@@ -265,7 +266,7 @@ def dequant_fp8(codes: torch.Tensor, scales: torch.Tensor, stream=None) -> torch
     if codes.dtype not in (torch.uint8, torch.float8_e4m3fn):
         raise TypeError("codes must be float8_e4m3fn or uint8")
     _need(scales, "scales", torch.float32, (rows, cols // 64))
-    w = _allocate(stream, lambda: torch.empty((rows, cols), dtype=BF16, device=codes.device))
+    w = _allocate(stream, torch.empty, (rows, cols), dtype=BF16, device=codes.device)
     _lib.check(_lib.dequant_fp8(_p(codes), _p(scales), rows, cols, _p(w), _stream(stream)), "lora_mlp_dequant_fp8")
     return w
 
@@ -607,7 +608,7 @@ def fold_gamma(w: MLPWeights, gamma: torch.Tensor, stream=None) -> MLPWeights:
         raise ValueError("gamma folds into bf16 frozen weights only")
     w.validate()
     _need(gamma, "gamma", BF16, (w.d,))
-    Wg, Wu = (_allocate(stream, lambda t=t: torch.empty_like(t)) for t in (w.Wg, w.Wu))
+    Wg, Wu = (_allocate(stream, torch.empty_like, t) for t in (w.Wg, w.Wu))
     _lib.check(_lib.block_fold_gamma(w.shape(1), w.c_struct(), _p(gamma), _p(Wg), _p(Wu), _stream(stream)),
                "lora_mlp_block_fold_gamma")
     return MLPWeights(Wg=Wg, Wu=Wu, Wd=w.Wd, Ag=w.Ag, Bg=w.Bg, Au=w.Au, Bu=w.Bu, Ad=w.Ad, Bd=w.Bd, alpha=w.alpha)
@@ -826,7 +827,7 @@ def embedding_forward(ids: torch.Tensor, E: torch.Tensor, *, scale: float = 1.0,
     if ids.dim() != 1 or E.dim() != 2:
         raise ValueError("ids must be [N] and E [V, d]")
     (N,), (V, d) = ids.shape, E.shape
-    out = _allocate(stream, lambda: E.new_empty((N, d))) if out is None else _need(out, "out", BF16, (N, d))
+    out = _allocate(stream, E.new_empty, (N, d)) if out is None else _need(out, "out", BF16, (N, d))
     _lib.check(_lib.embedding_forward(N, V, d, scale, _p(ids), _p(E), _p(out), _stream(stream)),
                "lora_embedding_forward")
     return out
@@ -849,7 +850,7 @@ def embedding_backward(dOut: torch.Tensor, ids: torch.Tensor, V: int, *, scale: 
         raise ValueError(f"padding_idx must be in [0, {V})")
     dev = dOut.device
     if dE is None:
-        dE = _allocate(stream, lambda: torch.empty((V, d), dtype=dtype, device=dev))
+        dE = _allocate(stream, torch.empty, (V, d), dtype=dtype, device=dev)
     else:
         _need(dE, "dE", dtype, (V, d))
     ws = _scratch(workspace, _lib.embedding_sizes(N, V, d), dev, stream)
@@ -930,7 +931,7 @@ def _heads_out(t, name, like, stream):
     """(t or a new contiguous tensor of `like`'s shape, its view)."""
     if t is not None:
         return t, _heads(t, name, like.shape, True)
-    t = _allocate(stream, lambda: torch.empty_like(like, memory_format=torch.contiguous_format))
+    t = _allocate(stream, torch.empty_like, like, memory_format=torch.contiguous_format)
     S, H, D = t.shape[-3:]
     return t, _lib.QKView(t.data_ptr(), S * H * D, H * D, D)
 
@@ -970,7 +971,8 @@ def qk_norm_rope_forward(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, si
     """(q_out, k_out): each head of q [B, S, Hq, D] and k [B, S, Hk, D] (or without B) normed (times q_gain, k_gain
     [D]; no norm without them) and turned by its position's angles, cos and sin fp32 [P, rot/2].  positions: int64
     [B, S] or [S], else 0 .. S-1.  Pairs are (i, i + rot/2), or (2i, 2i + 1) with interleaved; elements from rot on
-    do not turn.  q, k and given outputs may be strided views; new outputs are contiguous."""
+    do not turn.  q, k and given outputs may be strided views; new outputs are contiguous.  q_out may be q itself, and
+    k_out k (in place); outputs overlap nothing else."""
     shape, vq, vk, rest = _qk_call(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved)
     q_out, oq = _heads_out(q_out, "q_out", q, stream)
     k_out, ok = _heads_out(k_out, "k_out", k, stream)
@@ -983,14 +985,15 @@ def qk_norm_rope_backward(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, s
                           eps: float = 1e-6, interleaved: bool = False, gain_grads: bool = True, dq=None, dk=None,
                           workspace: Workspace | None = None, stream=None):
     """(dq, dk, dq_gain, dk_gain) from the forward's arguments and the gradients of its results; the gains'
-    gradients are fp32 [D], None without gains or with gain_grads=False (frozen gains)."""
+    gradients are fp32 [D], None without gains or with gain_grads=False (frozen gains).  dq may be dq_out itself or q,
+    and dk likewise; given outputs overlap nothing else."""
     shape, vq, vk, rest = _qk_call(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved)
     vdq_out, vdk_out = _heads(dq_out, "dq_out", q.shape), _heads(dk_out, "dk_out", k.shape)
     dq, vdq = _heads_out(dq, "dq", q, stream)
     dk, vdk = _heads_out(dk, "dk", k, stream)
     dgq = dgk = ws = None
     if q_gain is not None and gain_grads:
-        dgq, dgk = _allocate(stream, lambda: q.new_empty((2, shape.D), dtype=torch.float32)).unbind(0)
+        dgq, dgk = _allocate(stream, q.new_empty, (2, shape.D), dtype=torch.float32).unbind(0)
         ws = _scratch(workspace, _lib.qk_rope_sizes(shape), q.device, stream)
     _lib.check(_lib.qk_rope_backward(shape, vq, vk, *rest, vdq_out, vdk_out, vdq, vdk, _p(dgq), _p(dgk), _p(ws),
                                      0 if ws is None else ws.numel(), _stream(stream)), "lora_qk_rope_backward")
@@ -1065,7 +1068,7 @@ def _distill_out(logits, out, inplace, stream):
     if inplace:
         return logits
     if out is None:
-        return _allocate(stream, lambda: logits.new_empty_strided(logits.shape, logits.stride()))
+        return _allocate(stream, logits.new_empty_strided, logits.shape, logits.stride())
     if out.shape != logits.shape or out.stride() != logits.stride() or out.dtype != BF16 or not out.is_cuda:
         raise ValueError("out must have the logits' shape, strides and dtype")
     return out
@@ -1080,7 +1083,7 @@ def distill_forward(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_
     label (int64 [N], optional) is ignore_index and for rows without an entry."""
     shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
                                 ignore_index)
-    loss = _allocate(stream, lambda: logits.new_empty((shape.N,), dtype=torch.float32))
+    loss = _allocate(stream, logits.new_empty, (shape.N,), dtype=torch.float32)
     _lib.check(_lib.distill_forward(shape, *ptrs, _p(loss), _stream(stream)), "lora_distill_forward")
     return loss
 
@@ -1111,7 +1114,7 @@ def distill_loss(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ids
         raise ValueError("reduction must be 'sum' or 'mean'")
     shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
                                 ignore_index)
-    out = _allocate(stream, lambda: logits.new_empty((2,), dtype=torch.float32))
+    out = _allocate(stream, logits.new_empty, (2,), dtype=torch.float32)
     dlogits = _distill_out(logits, grad_out, inplace, stream) if with_grad else None
     ws = _scratch(workspace, _lib.distill_sizes(shape), logits.device, stream)
     _lib.check(_lib.distill_loss(shape, *ptrs, red, _p(out), _p(dlogits), _p(ws), ws.numel(), _stream(stream)),

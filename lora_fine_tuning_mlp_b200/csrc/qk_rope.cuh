@@ -211,8 +211,9 @@ __device__ __forceinline__ QkPlace<FLAT> qk_place(const QkArgs& a, const QkDivis
     return l;
 }
 
-// A warp takes a unit of queries or of keys.
-template <bool NORM, bool INTER, bool FLAT>
+// A warp takes a unit of queries or of keys.  IN_PLACE: results may lie over
+// what is read (a thread reads all of a head that it will write, and no other).
+template <bool NORM, bool INTER, bool FLAT, bool IN_PLACE>
 __global__ void __launch_bounds__(kQkThreads, NORM ? 4 : 8) qk_rope_kernel(const QkArgs a) {
     constexpr int U = NORM ? kQkUnroll : kQkRopeUnroll;
     uint32_t unit = blockIdx.x * kQkWarps + (threadIdx.x >> 5);
@@ -246,8 +247,8 @@ __global__ void __launch_bounds__(kQkThreads, NORM ? 4 : 8) qk_rope_kernel(const
         if (FLAT && u > 0) l = qk_place<FLAT, U>(a, by, H, unit, u), ip = l.head(in);
         v[u][0] = v[u][1] = make_uint4(0u, 0u, 0u, 0u);
         if (works && (FLAT ? l.in : l0.h + u * rows < H)) {
-            v[u][0] = load_once(ip + v0);
-            v[u][1] = load_once(ip + v1);
+            v[u][0] = load_once<IN_PLACE>(ip + v0);
+            v[u][1] = load_once<IN_PLACE>(ip + v1);
         }
         if (!FLAT) ip += rows * in.sh;
         if (FLAT || u == 0) p[FLAT ? u : 0] = l.position(a);
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kQkThreads, NORM ? 4 : 8) qk_rope_kernel(const
 // block's sums go to `part`, which qk_gain_kernel adds up in block order.
 constexpr int kQkBwdUnroll = 2;
 
-template <bool INTER, bool FLAT>
+template <bool INTER, bool FLAT, bool IN_PLACE>
 __global__ void __launch_bounds__(kQkThreads, kQkBwdBlocksPerSm) qk_rope_bwd_kernel(const QkArgs a) {
     __shared__ float sums[kQkWarps][512];
     const int kind = static_cast<int>(blockIdx.x) >= a.blocks_q;
@@ -344,10 +345,10 @@ __global__ void __launch_bounds__(kQkThreads, kQkBwdBlocksPerSm) qk_rope_bwd_ker
             vy[u][0] = vy[u][1] = vx[u][0] = vx[u][1] = make_uint4(0u, 0u, 0u, 0u);
             if (works && l[u].in) {
                 const uint4 *yp = l[u].head(dy), *xp = l[u].head(x);
-                vy[u][0] = load_once(yp + v0);
-                vy[u][1] = load_once(yp + v1);
-                vx[u][0] = load_once(xp + v0);
-                vx[u][1] = load_once(xp + v1);
+                vy[u][0] = load_once<IN_PLACE>(yp + v0);
+                vy[u][1] = load_once<IN_PLACE>(yp + v1);
+                vx[u][0] = load_once<IN_PLACE>(xp + v0);
+                vx[u][1] = load_once<IN_PLACE>(xp + v1);
             }
             if (FLAT || u == 0) p[FLAT ? u : 0] = l[u].position(a);
         }

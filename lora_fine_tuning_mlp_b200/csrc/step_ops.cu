@@ -474,6 +474,40 @@ int check_view(const lora_qk_view* v) {
     return reinterpret_cast<uintptr_t>(v->data) % 16 ? LORA_MLP_ERR_MISALIGNED : LORA_MLP_OK;
 }
 
+// A written view's strides nest: in ascending order, each is at least what the
+// axes before it span, so that no two of its elements are one.
+int check_written(const lora_qk_view* v, const lora_qk_shape* sh, int64_t heads) {
+    struct Axis {
+        uint64_t stride;
+        int64_t n;
+    } axes[3] = {{0, heads}, {0, sh->S}, {0, sh->B}};
+    const int64_t strides[3] = {v->stride_h, v->stride_s, v->stride_b};
+    for (int i = 0; i < 3; ++i)
+        axes[i].stride = strides[i] < 0 ? 0 - static_cast<uint64_t>(strides[i]) : static_cast<uint64_t>(strides[i]);
+    for (int i : {0, 1, 0})
+        if (axes[i].stride > axes[i + 1].stride) std::swap(axes[i], axes[i + 1]);
+    unsigned __int128 span = static_cast<uint64_t>(sh->D);
+    for (const Axis& x : axes) {
+        if (x.n == 1) continue;
+        if (x.stride < span) return LORA_MLP_ERR_UNSUPPORTED_SHAPE;
+        span += static_cast<unsigned __int128>(x.n - 1) * x.stride;
+    }
+    return LORA_MLP_OK;
+}
+
+// Two views that begin at one address: whether they are the same, stride by
+// stride (those of axes of one entry are never used).
+bool same_begin(const lora_qk_view* x, const lora_qk_view* y) { return x->data == y->data; }
+bool same_view(const lora_qk_view* x, const lora_qk_view* y, const lora_qk_shape* sh, int64_t heads) {
+    return (sh->B == 1 || x->stride_b == y->stride_b) && (sh->S == 1 || x->stride_s == y->stride_s) &&
+           (heads == 1 || x->stride_h == y->stride_h);
+}
+
+// `out` written in place of `in`, or not over its beginning.
+int check_in_place(const lora_qk_view* out, const lora_qk_view* in, const lora_qk_shape* sh, int64_t heads) {
+    return same_begin(out, in) && !same_view(out, in, sh, heads) ? LORA_MLP_ERR_INVALID_ARG : LORA_MLP_OK;
+}
+
 QkView qk_view(const lora_qk_view* v) {
     return {static_cast<uint4*>(v->data), v->stride_b / 8, v->stride_s / 8, v->stride_h / 8};
 }
@@ -521,17 +555,23 @@ QkArgs qk_args(const lora_qk_shape* sh, const void* q_gain, const void* k_gain, 
     return a;
 }
 
-template <bool FLAT>
+template <bool FLAT, bool IN_PLACE>
 auto pick_qk(bool norm, bool inter) {
-    return norm ? (inter ? qk_rope_kernel<true, true, FLAT> : qk_rope_kernel<true, false, FLAT>)
-                : (inter ? qk_rope_kernel<false, true, FLAT> : qk_rope_kernel<false, false, FLAT>);
+    return norm ? (inter ? qk_rope_kernel<true, true, FLAT, IN_PLACE> : qk_rope_kernel<true, false, FLAT, IN_PLACE>)
+                : (inter ? qk_rope_kernel<false, true, FLAT, IN_PLACE> : qk_rope_kernel<false, false, FLAT, IN_PLACE>);
+}
+template <bool IN_PLACE>
+auto pick_qk_bwd(bool inter, bool flat) {
+    return inter ? (flat ? qk_rope_bwd_kernel<true, true, IN_PLACE> : qk_rope_bwd_kernel<true, false, IN_PLACE>)
+                 : (flat ? qk_rope_bwd_kernel<false, true, IN_PLACE> : qk_rope_bwd_kernel<false, false, IN_PLACE>);
 }
 
 // Both passes without the norm, and the forward with it: one unit a warp.
-int launch_qk(const char* name, const QkArgs& a, bool norm, bool inter, cudaStream_t st) {
+int launch_qk(const char* name, const QkArgs& a, bool norm, bool inter, bool in_place, cudaStream_t st) {
     const int64_t units = int64_t{a.units[0]} + a.units[1];
     const int64_t blocks = (units + kQkWarps - 1) / kQkWarps;
-    auto kernel = a.flat ? pick_qk<true>(norm, inter) : pick_qk<false>(norm, inter);
+    auto kernel = in_place ? (a.flat ? pick_qk<true, true>(norm, inter) : pick_qk<false, true>(norm, inter))
+                           : (a.flat ? pick_qk<true, false>(norm, inter) : pick_qk<false, false>(norm, inter));
     return launch(name, kernel, dim3(static_cast<unsigned>(blocks)), kQkThreads, 0, st, false, 1, a);
 }
 
@@ -560,6 +600,11 @@ int lora_qk_rope_forward(const lora_qk_shape* shape, const lora_qk_view* q, cons
     for (const lora_qk_view* v : {q, k, q_out, k_out}) STEP_TRY(check_view(v));
     STEP_TRY(check_args({{cos, 16}, {sin, 16}}));
     STEP_TRY(check_optional({{q_gain, 16}, {k_gain, 16}, {positions, 8}}));
+    STEP_TRY(check_written(q_out, shape, shape->Hq));
+    STEP_TRY(check_written(k_out, shape, shape->Hk));
+    STEP_TRY(check_in_place(q_out, q, shape, shape->Hq));
+    STEP_TRY(check_in_place(k_out, k, shape, shape->Hk));
+    if (same_begin(q_out, k) || same_begin(k_out, q) || same_begin(q_out, k_out)) return LORA_MLP_ERR_INVALID_ARG;
     STEP_TRY(check_memory({{q->data, 16}, {k->data, 16}, {q_out->data, 16}, {k_out->data, 16}, {q_gain, 16},
                            {k_gain, 16}, {cos, 16}, {sin, 16}, {positions, 8}}));
     DevInfo di;
@@ -570,7 +615,8 @@ int lora_qk_rope_forward(const lora_qk_shape* shape, const lora_qk_view* q, cons
     a.in[1] = qk_view(k);
     a.out[0] = qk_view(q_out);
     a.out[1] = qk_view(k_out);
-    return launch_qk("QK_rope_fwd", a, q_gain != nullptr, shape->interleaved != 0, static_cast<cudaStream_t>(stream));
+    return launch_qk("QK_rope_fwd", a, q_gain != nullptr, shape->interleaved != 0,
+                     same_begin(q_out, q) || same_begin(k_out, k), static_cast<cudaStream_t>(stream));
 }
 
 int lora_qk_rope_sizes(const lora_qk_shape* shape, size_t* workspace_bytes) {
@@ -599,6 +645,16 @@ int lora_qk_rope_backward(const lora_qk_shape* shape, const lora_qk_view* q, con
         STEP_TRY(lora_qk_rope_sizes(shape, &need));
         if (workspace_bytes < need) return LORA_MLP_ERR_WORKSPACE_TOO_SMALL;
     }
+    STEP_TRY(check_written(dq, shape, shape->Hq));
+    STEP_TRY(check_written(dk, shape, shape->Hk));
+    STEP_TRY(check_in_place(dq, dq_out, shape, shape->Hq));
+    STEP_TRY(check_in_place(dk, dk_out, shape, shape->Hk));
+    if (same_begin(dq, dk_out) || same_begin(dk, dq_out) || same_begin(dq, dk)) return LORA_MLP_ERR_INVALID_ARG;
+    if (norm) {
+        STEP_TRY(check_in_place(dq, q, shape, shape->Hq));
+        STEP_TRY(check_in_place(dk, k, shape, shape->Hk));
+        if (same_begin(dq, k) || same_begin(dk, q)) return LORA_MLP_ERR_INVALID_ARG;
+    }
     STEP_TRY(check_memory({{norm ? q->data : nullptr, 16}, {norm ? k->data : nullptr, 16}, {dq_out->data, 16},
                            {dk_out->data, 16}, {dq->data, 16}, {dk->data, 16}, {q_gain, 16}, {k_gain, 16}, {cos, 16},
                            {sin, 16}, {positions, 8}, {dq_gain, 4}, {dk_gain, 4}, {gains ? workspace : nullptr, 16}}));
@@ -611,7 +667,9 @@ int lora_qk_rope_backward(const lora_qk_shape* shape, const lora_qk_view* q, con
     a.out[0] = qk_view(dq);
     a.out[1] = qk_view(dk);
     a.turn = -1.0f;
-    if (!norm) return launch_qk("QK_rope_bwd", a, false, shape->interleaved != 0, st);
+    const bool in_place = same_begin(dq, dq_out) || same_begin(dk, dk_out) ||
+                          (norm && (same_begin(dq, q) || same_begin(dk, k)));
+    if (!norm) return launch_qk("QK_rope_bwd", a, false, shape->interleaved != 0, in_place, st);
     a.x[0] = qk_view(q);
     a.x[1] = qk_view(k);
     a.part = gains ? static_cast<float*>(workspace) : nullptr;
@@ -619,8 +677,8 @@ int lora_qk_rope_backward(const lora_qk_shape* shape, const lora_qk_view* q, con
     qk_bwd_blocks(a, blocks);
     a.blocks_q = static_cast<int>(blocks[0]);
     const int all = static_cast<int>(blocks[0] + blocks[1]);
-    auto kernel = shape->interleaved ? (a.flat ? qk_rope_bwd_kernel<true, true> : qk_rope_bwd_kernel<true, false>)
-                                     : (a.flat ? qk_rope_bwd_kernel<false, true> : qk_rope_bwd_kernel<false, false>);
+    auto kernel = in_place ? pick_qk_bwd<true>(shape->interleaved != 0, a.flat != 0)
+                           : pick_qk_bwd<false>(shape->interleaved != 0, a.flat != 0);
     STEP_TRY(launch("QK_norm_rope_bwd", kernel,
                     dim3(static_cast<unsigned>(all)), kQkThreads, 0, st, false, 1, a));
     if (!gains) return LORA_MLP_OK;
