@@ -24,10 +24,18 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+# A Stream object costs 3 us a call; torch has the address without one under names that are not public.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    """The address of a stream, by default of the current device's current one (as torch.cuda.current_stream() has
-    it, without the Stream object, which costs 3 us a call)."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
+    """The address of a stream, by default of the current device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or _current_device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_current_device())
 
 
 def _need(t, name, dtype, shape=None):
