@@ -14,6 +14,7 @@ import functools
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -880,6 +881,7 @@ class EmbeddingFunction(torch.autograd.Function):
         return embedding_forward(ids, E, scale=scale)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dOut):
         (ids,) = ctx.saved_tensors
         V, scale, padding_idx = ctx.cfg
@@ -1028,6 +1030,7 @@ class QKNormRopeFunction(torch.autograd.Function):
                                     interleaved=interleaved)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, cos, sin, positions, q_gain, k_gain = ctx.saved_tensors
         eps, interleaved = ctx.cfg
@@ -1166,6 +1169,7 @@ class DistillFunction(torch.autograd.Function):
         return out[0]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         logits, teacher_logits, teacher_ids, labels, out = ctx.saved_tensors
         kw, inplace = ctx.cfg
