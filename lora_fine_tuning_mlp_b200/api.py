@@ -294,6 +294,7 @@ class LoRAMLPFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dOut):
         (X,) = ctx.saved_tensors
         dX, g = backward(X, ctx.w, ctx.saved_lr, dOut.contiguous())
@@ -541,6 +542,7 @@ class LoRALinearFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         (X,) = ctx.saved_tensors
         dX, dA, dB = linear_backward(X, ctx.w, ctx.saved_lr, dY.contiguous())
@@ -603,6 +605,7 @@ class RMSNormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, gamma, rstd = ctx.saved_tensors
         return rmsnorm_backward(x, gamma, rstd, dy.contiguous()), None, None
@@ -685,6 +688,7 @@ class LoRAMLPBlockFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dOut):
         (X,) = ctx.saved_tensors
         dX, g = block_backward(X, ctx.w, ctx.gamma, ctx.saved_lr, dOut.contiguous())
@@ -813,6 +817,7 @@ class CrossEntropyFunction(torch.autograd.Function):
         return out[0]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         logits, labels, lse, out = ctx.saved_tensors
         s, c, ign, inplace = ctx.cfg

@@ -1,4 +1,4 @@
-"""A second derivative through the operators around the dense layers is an error, not a term that is silently lost."""
+"""A second derivative through the autograd functions is an error, not a term that is silently lost."""
 import pytest
 import torch
 
@@ -36,7 +36,40 @@ def distillation():
     return z, api.DistillFunction.apply(z, torch.ones(3, 2, device="cuda"), ids)
 
 
-@pytest.mark.parametrize("make", [embedding, rotation, distillation])
+def mlp():
+    x, r, d, f = leaf(128, 64), 8, 64, 128
+    w = api.MLPWeights(*(leaf(*shape).detach() * 0.1 for shape in
+                         ((f, d), (f, d), (d, f), (r, d), (f, r), (r, d), (f, r), (r, f), (d, r))), alpha=16.0)
+    return x, w, (w.Ag, w.Bg, w.Au, w.Bu, w.Ad, w.Bd)
+
+
+def dense():
+    x, w, adapters = mlp()
+    return x, api.LoRAMLPFunction.apply(x, w, *adapters)
+
+
+def block():
+    x, w, adapters = mlp()
+    return x, api.LoRAMLPBlockFunction.apply(x, w, torch.ones(64, dtype=BF16, device="cuda"), 1e-5, *adapters)
+
+
+def projection():
+    x = leaf(128, 64)
+    w = api.LinearWeights(W=leaf(128, 64).detach(), A=leaf(8, 64).detach(), B=leaf(128, 8).detach(), alpha=16.0)
+    return x, api.LoRALinearFunction.apply(x, w, w.A, w.B)
+
+
+def norm():
+    x = leaf(128, 64)
+    return x, api.RMSNormFunction.apply(x, torch.ones(64, dtype=BF16, device="cuda"), 1e-5)
+
+
+def cross_entropy():
+    z = leaf(3, 40)
+    return z, api.CrossEntropyFunction.apply(z, torch.tensor([1, 2, 39], device="cuda"))
+
+
+@pytest.mark.parametrize("make", [embedding, rotation, distillation, dense, block, projection, norm, cross_entropy])
 def test_second_derivative(make):
     x, y = make()
     (y.float() ** 2).sum().backward(retain_graph=True)
