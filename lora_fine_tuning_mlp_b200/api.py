@@ -847,6 +847,11 @@ def embedding_forward(ids: torch.Tensor, E: torch.Tensor, *, scale: float = 1.0,
     return out
 
 
+def _check_padding(padding_idx, V):
+    if padding_idx is not None and not 0 <= padding_idx < V:
+        raise ValueError(f"padding_idx must be in [0, {V})")
+
+
 def embedding_backward(dOut: torch.Tensor, ids: torch.Tensor, V: int, *, scale: float = 1.0, padding_idx=None,
                        dtype=BF16, dE=None, workspace: Workspace | None = None, stream=None):
     """dE [V, d], the gradient of embedding_forward's table: each row the sum of its tokens' rows of dOut [N, d]
@@ -860,8 +865,7 @@ def embedding_backward(dOut: torch.Tensor, ids: torch.Tensor, V: int, *, scale: 
     kind = {BF16: _lib.EMBEDDING_GRAD_BF16, torch.float32: _lib.EMBEDDING_GRAD_FP32}.get(dtype)
     if kind is None:
         raise TypeError("dtype must be torch.bfloat16 or torch.float32")
-    if padding_idx is not None and not 0 <= padding_idx < V:
-        raise ValueError(f"padding_idx must be in [0, {V})")
+    _check_padding(padding_idx, V)
     dev = dOut.device
     if dE is None:
         dE = _allocate(stream, torch.empty, (V, d), dtype=dtype, device=dev)
@@ -880,6 +884,7 @@ class EmbeddingFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, ids, E, scale=1.0, padding_idx=None):
+        _check_padding(padding_idx, E.shape[0])
         ids = ids.contiguous()
         ctx.save_for_backward(ids)
         ctx.cfg = (E.shape[0], scale, padding_idx)
