@@ -14,7 +14,10 @@
  * Layout and types.  E, out and dOut are bf16, row-major, densely packed,
  * 16-byte aligned; ids are int64, 8-byte aligned; dE is bf16 or fp32 [V, d],
  * every row written.  N, V and d are at least 1, N and d at most 2^30 and V at
- * most 2^31 - 2; d is a multiple of 8.  Other conventions: lora_step.h.
+ * most 2^31 - 2; d is a multiple of 8.  The gradient's sort reads 2 KB for each
+ * pair of tiles of 4096 tokens in each pass: nothing beside dOut at a step's
+ * usual size, as long as the rest at some 10^7 tokens, and far longer at the
+ * limit.  Other conventions: lora_step.h.
  *
  * An id outside [0, V) is a device-side finding: its row of out is NaN, it
  * adds nothing to dE, and lora_step_device_status reports

@@ -576,7 +576,9 @@ int launch_qk(const char* name, const QkArgs& a, bool norm, bool inter, bool in_
 }
 
 // Blocks of the backward through the norm for queries and keys: together at
-// most kQkBwdBlocks, shared in proportion to their units.
+// most kQkBwdBlocks, shared in proportion to their units.  A B200's 148
+// multiprocessors are written out, as the workspace is sized by them, and
+// lora_qk_rope_sizes needs no device; where there are fewer, blocks wait.
 constexpr int64_t kQkBwdBlocks = 148 * kQkBwdBlocksPerSm;
 
 void qk_bwd_blocks(const QkArgs& a, int64_t (&blocks)[2]) {
