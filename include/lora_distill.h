@@ -38,7 +38,8 @@
  * distance from the row's largest, whatever the level of the logits.  With
  * softcapping 2^-22 cap / T is added up to cap = 128 T; above, t is formed to
  * fp32's precision first (2^-20 of the row's largest |t| / T), which takes about
- * 1.8 times as long.  Probabilities and gradients below 2^-126 may be 0.
+ * 1.8 times as long.  A row's loss is T^2 times a difference of such logarithms,
+ * and off by T^2 times as much.  Probabilities and gradients below 2^-126 may be 0.
  *
  * A teacher id below -1 or not below V is a device-side finding: the entry
  * counts as absent, the row's loss is NaN, and lora_step_device_status reports

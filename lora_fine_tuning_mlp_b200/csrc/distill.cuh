@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(T + 32 * kDsTeachers, T >= 512 ? 1 : T >= 256 
                     sum += p * ((t.tl[e] - t.log_psum) - (y * kLn2 - log_s));
                 }
                 sum = ds_warp_sum(sum);
-                if (lane == 0) a.loss[row] = t.bad ? __int_as_float(0x7fc00000) : (t.live ? a.T * a.T * sum : 0.0f);
+                if (lane == 0) a.loss[row] = t.bad ? __int_as_float(0x7fc00000) : (t.live ? a.T * (a.T * sum) : 0.0f);
             }
             if (t.bad && rank == 0 && lane == 0) atomicMin(a.status, kStatusBad);
             if (GRAD) {
