@@ -42,10 +42,13 @@
 // with tanhf).  Above it t itself is what exponents are taken of, to fp32's
 // precision of t, and rows are else treated as without softcapping.
 //
-// On a B200: 4096 rows of 128256 logits, loss and gradient, 454 us (4.6 TB/s; the
+// On a B200: 4096 rows of 128256 logits, loss and gradient, 455 us (4.6 TB/s; the
 // same stream of chunks merely copied takes 390, the exponentials' unit 248); the
-// loss of 2047 rows alone 106 us (4.9 TB/s); 1024 rows of 256000 with softcapping
-// 418 us, bound by the same unit's four operations a logit.
+// loss of 2047 rows alone 104 to 110 us (4.9 TB/s); 1024 rows of 256000 with
+// softcapping 415 us.  There the unit has 4.5 operations a logit in the two
+// passes, 280 us if all multiprocessors did nothing else: clusters of four leave
+// 16 of 148 idle (312 us), and on the others it is 73 % busy, the rest being
+// waits for results of fixed latency and for its queue.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
