@@ -161,9 +161,9 @@ class Workspace:
 
 
 def _allocate(stream, make, *args, **kw):
-    """make(*args, **kw), memory for a call that runs on `stream`.  It comes from that stream's part of the allocator: what the
-    current stream's part hands out may still be in use by work queued there, which `stream` does not wait for.  The
-    caller goes on with it on the current stream, which the allocator is told."""
+    """make(*args, **kw), memory for a call that runs on `stream`.  It comes from that stream's part of the allocator:
+    what the current stream's part hands out may still be in use by work queued there, which `stream` does not wait
+    for.  The caller goes on with it on the current stream, which the allocator is told."""
     if stream is None:
         return make(*args, **kw)
     here = torch.cuda.current_stream(stream.device)
@@ -180,9 +180,10 @@ def _scratch(workspace, nbytes: int, device, stream):
             return torch.empty(nbytes, dtype=torch.uint8, device=device)
         with torch.cuda.stream(stream):
             return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is None:
+        return workspace.get(nbytes, device)
     buf = _allocate(stream, workspace.get, nbytes, device)
-    if stream is not None:
-        buf.record_stream(stream)  # it may come from an earlier call on another one
+    buf.record_stream(stream)  # it may come from an earlier call on another one
     return buf
 
 
@@ -841,7 +842,10 @@ def embedding_forward(ids: torch.Tensor, E: torch.Tensor, *, scale: float = 1.0,
     if ids.dim() != 1 or E.dim() != 2:
         raise ValueError("ids must be [N] and E [V, d]")
     (N,), (V, d) = ids.shape, E.shape
-    out = _allocate(stream, E.new_empty, (N, d)) if out is None else _need(out, "out", BF16, (N, d))
+    if out is None:
+        out = E.new_empty((N, d)) if stream is None else _allocate(stream, E.new_empty, (N, d))
+    else:
+        _need(out, "out", BF16, (N, d))
     _lib.check(_lib.embedding_forward(N, V, d, scale, _p(ids), _p(E), _p(out), _stream(stream)),
                "lora_embedding_forward")
     return out
@@ -951,7 +955,9 @@ def _heads_out(t, name, like, stream):
     """(t or a new contiguous tensor of `like`'s shape, its view)."""
     if t is not None:
         return t, _heads(t, name, like.shape, True)
-    t = _allocate(stream, torch.empty_like, like, memory_format=torch.contiguous_format)
+    dense = torch.contiguous_format
+    t = (torch.empty_like(like, memory_format=dense) if stream is None
+         else _allocate(stream, torch.empty_like, like, memory_format=dense))
     S, H, D = t.shape[-3:]
     return t, _lib.QKView(t.data_ptr(), S * H * D, H * D, D)
 
@@ -1013,7 +1019,9 @@ def qk_norm_rope_backward(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, s
     dk, vdk = _heads_out(dk, "dk", k, stream)
     dgq = dgk = ws = None
     if q_gain is not None and gain_grads:
-        dgq, dgk = _allocate(stream, q.new_empty, (2, shape.D), dtype=torch.float32).unbind(0)
+        both = (2, shape.D)
+        dgq, dgk = (q.new_empty(both, dtype=torch.float32) if stream is None
+                    else _allocate(stream, q.new_empty, both, dtype=torch.float32)).unbind(0)
         ws = _scratch(workspace, _lib.qk_rope_sizes(shape), q.device, stream)
     _lib.check(_lib.qk_rope_backward(shape, vq, vk, *rest, vdq_out, vdk_out, vdq, vdk, _p(dgq), _p(dgk), _p(ws),
                                      0 if ws is None else ws.numel(), _stream(stream)), "lora_qk_rope_backward")
@@ -1089,7 +1097,8 @@ def _distill_out(logits, out, inplace, stream):
     if inplace:
         return logits
     if out is None:
-        return _allocate(stream, logits.new_empty_strided, logits.shape, logits.stride())
+        n = logits.shape, logits.stride()
+        return logits.new_empty_strided(*n) if stream is None else _allocate(stream, logits.new_empty_strided, *n)
     if out.shape != logits.shape or out.stride() != logits.stride() or out.dtype != BF16 or not out.is_cuda:
         raise ValueError("out must have the logits' shape, strides and dtype")
     return out
@@ -1135,7 +1144,8 @@ def distill_loss(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ids
         raise ValueError("reduction must be 'sum' or 'mean'")
     shape, ptrs = _distill_call(logits, teacher_logits, teacher_ids, labels, temperature, logit_scale, softcap,
                                 ignore_index)
-    out = _allocate(stream, logits.new_empty, (2,), dtype=torch.float32)
+    out = (logits.new_empty((2,), dtype=torch.float32) if stream is None
+           else _allocate(stream, logits.new_empty, (2,), dtype=torch.float32))
     dlogits = _distill_out(logits, grad_out, inplace, stream) if with_grad else None
     ws = _scratch(workspace, _lib.distill_sizes(shape), logits.device, stream)
     _lib.check(_lib.distill_loss(shape, *ptrs, red, _p(out), _p(dlogits), _p(ws), ws.numel(), _stream(stream)),

@@ -33,14 +33,14 @@
 // kept for other rows.  Either way an exponent is off by 2^-23 of its distance
 // from the reference, which is fp32's own precision of it.
 //
-// With softcapping, t = cap tanh(s z / cap)
-// = cap - 2 cap r with r = 1 / (1 + e), e = 2^(cap2 z): exponents are taken of
-// -r, dt/dz = 4 s e r^2 has no cancellation where tanh saturates on either side,
-// and four logits share one reciprocal.  t / T is off by 2^-22 cap / T so,
-// however small t is: fp32 holds r, near 1/2, to 2^-24.  That is a choice for
-// speed up to cap / T = 128 (3e-5; 1024 rows of 256000 take 415 us so, 746 us
-// with tanhf).  Above it t itself is what exponents are taken of, to fp32's
-// precision of t, and rows are else treated as without softcapping.
+// With softcapping, t = cap tanh(s z / cap) = cap - 2 cap r with r = 1 / (1 + e),
+// e = 2^(cap2 z): exponents are taken of -r, dt/dz = 4 s e r^2 has no
+// cancellation where tanh saturates on either side, and four logits share one
+// reciprocal.  t / T is off by 2^-22 cap / T so, however small t is: fp32 holds
+// r, near 1/2, to 2^-24.  That is a choice for speed up to cap / T = 128 (3e-5;
+// 1024 rows of 256000 take 415 us so, 746 us with tanhf).  Above it t itself is
+// what exponents are taken of, to fp32's precision of t, and rows are else
+// treated as without softcapping.
 //
 // On a B200: 4096 rows of 128256 logits, loss and gradient, 455 us (4.6 TB/s; the
 // same stream of chunks merely copied takes 390, the exponentials' unit 248); the
